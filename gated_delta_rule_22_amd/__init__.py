@@ -1,6 +1,7 @@
 """Kimi Delta Attention hot path on MI355X: thin Python binding of libkda.so.
 
-The functions below carry the C ABI's names (``include/kda.h``) and only
+The functions carry the C ABI's names (``include/kda.h``; those of the serving
+step, ``include/kda_serve.h``, are in ``serve.py``) and only
 marshal arguments: they check devices, dtypes, shapes and contiguity, allocate
 outputs with torch when the caller gives none, and pass raw device pointers
 and the current HIP stream. Every step of the computation runs in the HIP
@@ -21,6 +22,9 @@ __all__ = [
     "kda_prefill_varlen", "kda_decode_step", "kda_decode_multi", "kda_prefill_layer",
     "kda_decode_layer", "KDA_GATE_LOG", "KDA_GATE_BOUNDED", "KDA_GATE_SCALAR",
     "kda_prefill_fwd_noalloc", "KDA_NOALLOC_SCRATCH_BYTES",
+    "kda_page_plan_workspace_size", "kda_page_plan", "kda_cache_append",
+    "kda_attn_paged_workspace_size", "kda_attn_paged", "kda_draft_verify_workspace_size",
+    "kda_draft_verify", "KDA_PLAN_OK", "KDA_PLAN_INVALID", "KDA_PLAN_NO_SLOTS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -85,6 +89,7 @@ def load_library():
     lib.kda_prefill_fwd_noalloc.argtypes = [vp, vp, vp, fp, fp, fp, vp, fp, i, i, i, i, i, i, i,
                                             vp]
     lib.kda_prefill_fwd_noalloc.restype = i
+    serve.declare(lib)
     _lib = lib
     return lib
 
@@ -454,3 +459,10 @@ def kda_decode_layer(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gate: to
     if st != 0:
         raise KDAError(st, "kda_decode_layer")
     return o
+
+
+from . import serve  # noqa: E402  (uses the helpers above)
+from .serve import (  # noqa: E402
+    KDA_PLAN_INVALID, KDA_PLAN_NO_SLOTS, KDA_PLAN_OK, kda_attn_paged,
+    kda_attn_paged_workspace_size, kda_cache_append, kda_draft_verify,
+    kda_draft_verify_workspace_size, kda_page_plan, kda_page_plan_workspace_size)

@@ -7,6 +7,7 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
+CSRC_SERVE = os.path.join(HERE, "csrc_serve")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libkda.so")
 BUILD = os.path.join(HERE, "_build")
@@ -17,15 +18,22 @@ FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
     # keep the compiler from emitting packed fp32 instructions
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+    "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-I", CSRC_SERVE,
 ]
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_prefill_generic.hip", "kda_prefill_mfma.hip",
-           "kda_varlen.hip", "kda_epilogue.hip", "kda_decode_multi_mfma.hip"]
+           "kda_varlen.hip", "kda_epilogue.hip", "kda_decode_multi_mfma.hip",
+           "kda_serve_api.cpp", "kda_page_plan.hip", "kda_cache_append.hip",
+           "kda_attn_paged.hip", "kda_draft_verify.hip"]
+
+
+def _path(src: str) -> str:
+    p = os.path.join(CSRC, src)
+    return p if os.path.exists(p) else os.path.join(CSRC_SERVE, src)
 
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-    cmd = [HIPCC, *FLAGS, "-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC, *FLAGS, "-x", "hip", "-c", _path(src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{r.stderr}")

@@ -1,90 +1,635 @@
 // Causal attention of new tokens over a paged cache.
 //
-// One wave per (token, query head): 64 keys at a time, one per lane, with the
-// running maximum and sum of the softmax in fp32, then the weighted values
-// with the head dimension over the lanes.
-#include "kda_serve_launch.h"
+// With s_j = scale q.k_j over a row's visible positions, m = max s_j and
+// l = sum exp(s_j - m): o = sum exp(s_j - m) v_j / l. One pass over the keys
+// keeps m, l and the unnormalised row; a new maximum m' scales l and the row
+// by exp(m - m'). Results over disjoint parts of the keys join by the same
+// rule. Scores are kept in the log2 domain (s log2 e), so that the
+// exponential is one v_exp_f32.
+//
+// attn_stream_*: decode steps and drafts, up to 32 rows per KV head. What
+// bounds them is reading K and V once. A workgroup takes one tile of 16 RT
+// rows and a part of its keys (kda_attn_sched.h); its four waves take 32
+// (fp32: 16) keys each in turn and run free of each other, so that every wave
+// has its next keys and values in flight while it computes. Their rows are
+// joined through LDS at the end.
+#include "kda_attn_sched.h"
 
 namespace kda {
 namespace {
 
-template <typename T, int D>
-__global__ __launch_bounds__(64) void attn_rows_kernel(AttnArgs a) {
-    const int t = blockIdx.x, hq = blockIdx.y, lane = threadIdx.x;
-    // the request of row t (the first whose rows hold it)
-    int req = -1, at = 0;
-    for (int i = 0; i < a.B && req < 0; ++i) {
-        int lo = a.cu[i], hi = a.cu[i + 1];
-        lo = lo < 0 ? 0 : (lo > a.T ? a.T : lo);
-        hi = hi < 0 ? 0 : (hi > a.T ? a.T : hi);
-        if (t >= lo && t < hi) { req = i; at = t - lo; }
-    }
-    if (req < 0) return;
-    const int h = hq / (a.Hq / a.Hkv);
-    const long cap = (long)a.width << a.page_shift;
-    long kept = a.kept[req];
-    kept = kept < 0 ? 0 : kept;
-    const long end = kept + at + 1 < cap ? kept + at + 1 : cap;
-    const int page = 1 << a.page_shift;
-    const T* q = (const T*)a.q + ((long)t * a.Hq + hq) * D;
-    float m = -INFINITY, l = 0.f, acc[(D + 63) / 64] = {};
-    for (long k0 = 0; k0 < end; k0 += 64) {
-        const long pos = k0 + lane;
-        long row = -1;
-        if (pos < end) {
-            const int pg = a.table[(long)req * a.width + (pos >> a.page_shift)];
-            if ((unsigned)pg < (unsigned)a.pool)
-                row = (((long)pg * a.Hkv + h) << a.page_shift) + (pos & (page - 1));
-        }
-        float s = -INFINITY;
-        if (row >= 0) {
-            s = 0.f;
-            const T* k = (const T*)a.kc + row * D;
-            for (int i = 0; i < D; ++i) s += to_f32(q[i]) * to_f32(k[i]);
-            s *= a.scale;
-        }
-        float mx = s;
-        for (int o = 32; o; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
-        const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
-        const float p = row >= 0 ? __expf(s - mu) : 0.f, c = __expf(m - mu);
-        float sum = p;
-        for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
-        l = l * c + sum;
-        m = mn;
-        for (int j = 0; j < (D + 63) / 64; ++j) acc[j] *= c;
-        for (int i = 0; i < 64; ++i) {
-            const long r = __shfl(row, i);
-            const float w = __shfl(p, i);
-            if (r < 0) continue;
-            for (int j = 0; j < (D + 63) / 64; ++j)
-                if (j * 64 + lane < D) acc[j] += w * to_f32(((const T*)a.vc)[r * D + j * 64 + lane]);
-        }
-    }
-    T* o = (T*)a.o + ((long)t * a.Hq + hq) * D;
-    for (int j = 0; j < (D + 63) / 64; ++j)
-        if (j * 64 + lane < D) o[j * 64 + lane] = from_f32<T>(l > 0.f ? acc[j] / l : (l == 0.f ? 0.f : l));
-    if (a.lse && lane == 0) a.lse[(long)t * a.Hq + hq] = l == 0.f ? -INFINITY : m + logf(l);
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
+constexpr int kKeepAll = 1 << 30;
+
+__device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ bool finite_bits(float x) {
+    return (__builtin_bit_cast(uint32_t, x) & 0x7f800000u) != 0x7f800000u;
+}
+__device__ __forceinline__ f32x4 mma4(float a, float b, f32x4 c) {
+    // D(16x16) += A(16x4) B(4x16), fp32: lane l holds A[l%16][l/16], B[l/16][l%16]
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-template <typename T>
-void launch(const AttnArgs& a, hipStream_t st) {
-    const dim3 g((unsigned)a.T, (unsigned)a.Hq);
-    switch (a.d) {
-        case 16: attn_rows_kernel<T, 16><<<g, 64, 0, st>>>(a); break;
-        case 32: attn_rows_kernel<T, 32><<<g, 64, 0, st>>>(a); break;
-        case 64: attn_rows_kernel<T, 64><<<g, 64, 0, st>>>(a); break;
-        default: attn_rows_kernel<T, 128><<<g, 64, 0, st>>>(a); break;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// Largest over the four lanes l % 16 + {0, 16, 32, 48}.
+__device__ __forceinline__ float max_quarters(float x) {
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float sum_quarters(float x) {
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
+// Row r of a request: packed row and query head.
+struct RowAt { bool in; long q; int t; };
+__device__ __forceinline__ RowAt row_at(const AttnArgs& a, const AttnItem& it, int G, int r) {
+    const unsigned t = (unsigned)r / (unsigned)G;
+    RowAt x;
+    x.in = (int)t < it.n;
+    x.t = (int)t;
+    x.q = (long)(it.row0 + (x.in ? (int)t : 0)) * a.Hq + it.h * G + (int)((unsigned)r - t * (unsigned)G);
+    return x;
+}
+
+// Result of a row, from its unnormalised values: 8 (bf16) or 4 (fp32) of them.
+__device__ __forceinline__ void store_row(bf16* o, const float* v, float inv) {
+    bf16x8 x;
+    for (int i = 0; i < 8; ++i) x[i] = (bf16)(v[i] * inv);
+    *(bf16x8*)o = x;
+}
+__device__ __forceinline__ void store_row(float* o, const float* v, float inv) {
+    for (int j = 0; j < 8; j += 4) {
+        f32x4 x;
+        for (int i = 0; i < 4; ++i) x[i] = v[j + i] * inv;
+        *(f32x4*)(o + j) = x;
     }
+}
+
+// Joins the four waves' rows: ml[wave][16][2] and acc[wave][16][D + 4] in LDS
+// hold 16 rows of each; writes the rows themselves, or a partial result.
+template <typename T, int D>
+__device__ __forceinline__ void join_waves(const AttnArgs& a, const AttnSplit& s,
+                                           const AttnItem& it, int G, int r0, const float* ml,
+                                           const float* acc) {
+    constexpr int kPer = 8, kLanes = D / kPer;      // 2 .. 16 threads per row
+    const int row = threadIdx.x / kLanes, d = threadIdx.x % kLanes * kPer;
+    if (row >= 16) return;
+    float m = -INFINITY, l = 0.f, v[kPer] = {};
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, ml[(w * 16 + row) * 2]);
+    for (int w = 0; w < 4; ++w) {
+        const float mw = ml[(w * 16 + row) * 2], lw = ml[(w * 16 + row) * 2 + 1];
+        if (lw == 0.f) continue;                    // that wave saw no key of this row
+        const float c = mw == -INFINITY ? 1.f : exp2_f(mw - m);   // (all scores NaN: lw is)
+        l += c * lw;
+        const float* x = acc + (w * 16 + row) * (D + 4) + d;
+        for (int i = 0; i < kPer; ++i) v[i] += c * x[i];
+    }
+    const int r = it.tile * s.R + r0 + row;
+    if (it.parts > 1) {
+        const long slot = it.slot + ((long)it.part * it.tiles + it.tile) * a.Hkv + it.h;
+        if (slot >= s.slots) return;                // offsets that decrease: see attn_req
+        const long at = slot * s.R + r0 + row;
+        for (int i = 0; i < kPer; i += 4)
+            *(f32x4*)(s.acc + at * D + d + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+        if (d == 0) { s.ml[at * 2] = m; s.ml[at * 2 + 1] = l; }
+        return;
+    }
+    const RowAt x = row_at(a, it, G, r);
+    if (!x.in) return;
+    store_row((T*)a.o + x.q * D + d, v, l == 0.f ? 0.f : 1.f / l);
+    if (a.lse && d == 0) a.lse[x.q] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+}
+
+// Range of keys of a part, and what of it needs a mask.
+struct Keys {
+    int begin, end;      // the part's positions
+    int all;             // positions below are visible to every row of the tile
+};
+__device__ __forceinline__ Keys part_keys(const AttnArgs& a, const AttnSplit& s,
+                                          const AttnItem& it, int G) {
+    const int cap = a.width << a.page_shift;
+    const int rows = it.n * G, r0 = it.tile * s.R, r1 = min(r0 + s.R, rows) - 1;
+    Keys k;
+    k.begin = it.part * it.C;
+    const int last = (int)((unsigned)r1 / (unsigned)G), first = (int)((unsigned)r0 / (unsigned)G);
+    k.end = (int)min(min((long)k.begin + it.C, (long)it.kept + last + 1), (long)cap);
+    k.all = (int)min((long)it.kept + first + 1, (long)cap);
+    return k;
+}
+
+// Page id of the 16 positions at pos (a multiple of 16), -1 when there is none.
+__device__ __forceinline__ int page_at(const AttnArgs& a, const int* table, int pos, int end) {
+    if (pos >= end) return -1;
+    const int p = uniform(table[pos >> a.page_shift]);
+    return (unsigned)p < (unsigned)a.pool ? p : -1;
+}
+
+// The running maximum, sum and rows of 16 RT rows in one wave. Lane l holds
+// row l % 16 of each group of 16 throughout; l is a sum over the lane's own
+// keys until finish().
+//
+// bf16: D x 32 keys a step. S^T = K Q^T leaves lane l with the scores of its
+// row against keys 16 sub + 4 (l / 16) + i; as the second operand of
+// O^T += V^T P^T they stay in place when the contraction runs over the keys in
+// that same order, which the transposing LDS read gives V.
+template <int D, int RT>
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, AttnSplit s) {
+    constexpr int KS = D < 32 ? 1 : D / 32;          // steps of 32 over the head
+    constexpr int NB = D / 16;                       // value columns in 16s
+    constexpr int VL = D / 16;                       // 16-byte loads per lane for 32 rows of V
+    constexpr int CH = D / 8;                        // 16-byte pieces of a row
+    __shared__ AttnSchedLds sched;
+    __shared__ __align__(16) float join[4 * 16 * (D + 4) > 4 * 32 * D / 2 ? 4 * 16 * (D + 4)
+                                                                         : 4 * 32 * D / 2];
+    __shared__ float join_ml[4 * 16 * 2];
+    const AttnItem it0 = attn_item<false>(a, s, blockIdx.x, sched);
+    AttnItem it = it0;
+    it.found = uniform(it0.found);
+    if (!it.found) return;
+    it.req = uniform(it.req); it.h = uniform(it.h); it.tile = uniform(it.tile);
+    it.part = uniform(it.part); it.parts = uniform(it.parts); it.tiles = uniform(it.tiles);
+    it.row0 = uniform(it.row0); it.n = uniform(it.n); it.kept = uniform(it.kept);
+    it.C = uniform(it.C);
+    const int G = a.Hq / a.Hkv, wave = wave_id(), lane = threadIdx.x & 63;
+    const int c16 = lane & 15, g4 = lane >> 4;
+    const Keys keys = part_keys(a, s, it, G);
+    const int* table = a.table + (long)it.req * a.width;
+    const float scale = a.scale * kLog2e;
+    bf16* stage = (bf16*)join + wave * (32 * D);     // V of this wave's 32 keys
+
+    bf16x8 qf[RT][KS];
+    int limit[RT];                                   // last visible position of the lane's row
+    for (int rt = 0; rt < RT; ++rt) {
+        const RowAt x = row_at(a, it, G, it.tile * s.R + rt * 16 + c16);
+        limit[rt] = x.in ? (int)min((long)it.kept + x.t, (long)kKeepAll) : -1;
+        const bf16* q = (const bf16*)a.q + x.q * D;
+        for (int k = 0; k < KS; ++k) {
+            const int d = 32 * k + 8 * g4;
+            bf16x8 z = {};
+            if (x.in && d < D) z = *(const bf16x8*)(q + d);
+            qf[rt][k] = z;
+        }
+    }
+
+    float m[RT], l[RT];
+    f32x4 acc[RT][NB];
+    for (int rt = 0; rt < RT; ++rt) {
+        m[rt] = -INFINITY;
+        l[rt] = 0.f;
+        for (int b = 0; b < NB; ++b) acc[rt][b] = zero4();
+    }
+
+    bf16x8 kf[2][KS], vf[VL];
+    int page[2], page_next[2];
+    const int row_mask = (1 << a.page_shift) - 1;
+    auto base_of = [&](int p, int pos) {             // row of the plane of head h
+        return (((long)p * a.Hkv + it.h) << a.page_shift) + (pos & row_mask);
+    };
+    auto load_k = [&](int pos) {
+        for (int u = 0; u < 2; ++u) {
+            if (page[u] >= 0) {
+                const bf16* k = (const bf16*)a.kc + (base_of(page[u], pos + 16 * u) + c16) * D;
+                for (int i = 0; i < KS; ++i)
+                    if (D >= 32 || g4 < 2) kf[u][i] = *(const bf16x8*)(k + 32 * i + 8 * g4);
+            } else {
+                for (int i = 0; i < KS; ++i) kf[u][i] = bf16x8{};
+            }
+        }
+    };
+    // piece i * 64 + lane of the 32 rows; a half (16 rows) is VL / 2 loads,
+    // but one load for D = 16
+    auto load_v = [&](int pos) {
+        for (int i = 0; i < VL; ++i) {
+            const int x = i * 64 + lane, key = x / CH, c = x % CH;
+            if (VL > 1) {
+                const int u = i >= VL / 2;
+                if (page[u] >= 0)
+                    vf[i] = *(const bf16x8*)((const bf16*)a.vc +
+                                             (base_of(page[u], pos + 16 * u) + (key & 15)) * D + 8 * c);
+                else
+                    vf[i] = bf16x8{};
+            } else {
+                const int p = key < 16 ? page[0] : page[1];
+                vf[i] = bf16x8{};
+                if (p >= 0)
+                    vf[i] = *(const bf16x8*)((const bf16*)a.vc +
+                                             (base_of(p, pos + (key & 16)) + (key & 15)) * D + 8 * c);
+            }
+        }
+    };
+    if (D == 16)
+        for (int u = 0; u < 2; ++u) kf[u][0] = bf16x8{};
+
+    int pos = keys.begin + wave * 32;
+    page[0] = page_at(a, table, pos, keys.end);
+    page[1] = page_at(a, table, pos + 16, keys.end);
+    if (pos < keys.end) {
+        load_k(pos);
+        load_v(pos);
+    }
+    for (; pos < keys.end; pos += 128) {
+        const int next = pos + 128;
+        page_next[0] = page_at(a, table, next, keys.end);
+        page_next[1] = page_at(a, table, next + 16, keys.end);
+        const bool gap0 = page[0] < 0, gap1 = page[1] < 0;
+        f32x4 st[RT][2];
+        for (int rt = 0; rt < RT; ++rt)
+            for (int u = 0; u < 2; ++u) {
+                f32x4 x = zero4();
+                for (int k = 0; k < KS; ++k) x = mma32(kf[u][k], qf[rt][k], x);
+                st[rt][u] = x;
+            }
+        // V rows that no row of the tile sees hold anything: they count 0
+        if (pos + 32 > keys.end) {
+            for (int i = 0; i < VL; ++i)
+                if (pos + (i * 64 + lane) / CH >= keys.end) vf[i] = bf16x8{};
+        }
+        // Positions that only some rows see: a value there that is not finite
+        // must not meet the weight 0 of the others in a product.
+        bool odd = false;
+        if (pos + 32 > keys.all) {
+            for (int i = 0; i < VL; ++i)
+                for (int j = 0; j < 8; ++j) odd |= !finite_bits((float)vf[i][j]);
+            odd = __any(odd);
+        }
+        lds_fence_wave();                            // last step's reads of the stage are done
+        for (int i = 0; i < VL; ++i) {
+            const int x = i * 64 + lane, key = x / CH, c = x % CH;
+            // a 16-lane transposing read takes 32 bytes of four rows: rows of
+            // 128 bytes and more put them 32 bytes apart
+            const int sw = D >= 64 ? c ^ (2 * (key & 3)) : c;
+            *(bf16x8*)(stage + key * D + 8 * sw) = vf[i];
+        }
+        const int p0 = page[0], p1 = page[1];
+        page[0] = page_next[0];
+        page[1] = page_next[1];
+        if (next < keys.end) {
+            load_k(next);
+            load_v(next);
+        }
+        bf16x8 pf[RT];
+        float pe[RT][2][4];
+        for (int rt = 0; rt < RT; ++rt) {
+            float x[2][4];
+            for (int u = 0; u < 2; ++u)
+                for (int i = 0; i < 4; ++i) x[u][i] = st[rt][u][i] * scale;
+            if (pos + 32 > keys.all || gap0 || gap1) {
+                for (int u = 0; u < 2; ++u)
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = pos + 16 * u + 4 * g4 + i;
+                        if (key > limit[rt] || key >= keys.end || (u ? gap1 : gap0)) x[u][i] = -INFINITY;
+                    }
+            }
+            float mx = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
+                             fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
+            mx = max_quarters(mx);
+            if (__any(mx > m[rt])) {
+                const float mn = fmaxf(m[rt], mx);
+                const float c = mn == -INFINITY ? 1.f : exp2_f(m[rt] - mn);
+                m[rt] = mn;
+                l[rt] *= c;
+                for (int b = 0; b < NB; ++b) acc[rt][b] *= c;
+            }
+            const float mu = m[rt] == -INFINITY ? 0.f : m[rt];
+            float sum = 0.f;
+            for (int u = 0; u < 2; ++u)
+                for (int i = 0; i < 4; ++i) {
+                    const float p = exp2_f(x[u][i] - mu);
+                    sum += p;
+                    pe[rt][u][i] = p;
+                }
+            l[rt] += sum;
+            // the weights are rounded to bf16 for the matrix cores (2^-9 on
+            // average); l sums them unrounded
+            pf[rt] = pack8(f32x4{pe[rt][0][0], pe[rt][0][1], pe[rt][0][2], pe[rt][0][3]},
+                           f32x4{pe[rt][1][0], pe[rt][1][1], pe[rt][1][2], pe[rt][1][3]});
+        }
+        lds_fence_wave();                            // the stage is written
+        for (int b = 0; b < NB; ++b) {
+            s16x4 lo, hi;
+            {
+                const int key = 4 * g4 + c16 / 4, c = 2 * b + (c16 & 3) / 2;
+                const int sw = D >= 64 ? c ^ (2 * (key & 3)) : c;
+                const bf16* x = stage + key * D + 8 * sw + 4 * (c16 & 1);
+                lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)x);
+                hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(x + 16 * D));
+            }
+            bf16x8 va = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            if (odd)
+                for (int j = 0; j < 8; ++j)
+                    if (!finite_bits((float)va[j])) va[j] = (bf16)0.f;
+            for (int rt = 0; rt < RT; ++rt) acc[rt][b] = mma32(va, pf[rt], acc[rt][b]);
+        }
+        if (odd) {
+            // the values left out above, for the rows that see them
+            for (int key = 0; key < 32; ++key) {
+                const int p = key < 16 ? p0 : p1;
+                if (p < 0 || pos + key >= keys.end) continue;
+                const bf16* v = (const bf16*)a.vc + base_of(p, pos + (key & 16)) * D + (long)(key & 15) * D;
+                for (int rt = 0; rt < RT; ++rt) {
+                    float w = 0.f;
+                    for (int u = 0; u < 2; ++u)
+                        for (int i = 0; i < 4; ++i)
+                            if (u == key / 16 && i == (key & 3)) w = pe[rt][u][i];
+                    w = __shfl(w, c16 + 16 * ((key & 15) / 4));
+                    const bool sees = pos + key <= limit[rt];
+                    for (int b = 0; b < NB; ++b)
+                        for (int i = 0; i < 4; ++i) {
+                            const float x = (float)v[16 * b + 4 * g4 + i];
+                            if (sees && !finite_bits(x)) acc[rt][b][i] += w * x;
+                        }
+                }
+            }
+        }
+    }
+
+    for (int rt = 0; rt < RT; ++rt) {
+        const float sum = sum_quarters(l[rt]);
+        __syncthreads();                             // stage and the last group's rows are free
+        if (g4 == 0) {
+            join_ml[(wave * 16 + c16) * 2] = m[rt];
+            join_ml[(wave * 16 + c16) * 2 + 1] = sum;
+        }
+        for (int b = 0; b < NB; ++b)
+            *(f32x4*)(join + (wave * 16 + c16) * (D + 4) + 16 * b + 4 * g4) = acc[rt][b];
+        __syncthreads();
+        join_waves<bf16, D>(a, s, it, G, rt * 16, join_ml, join);
+    }
+}
+
+// fp32, 16 keys a step. The contraction over the head takes element
+// g D / 4 + s of the lane quarter g in step s, so that a lane's part of a key
+// is contiguous; O^T's row 4 g + i of block c is value column (4 g + i) D / 16
+// + c, so that a lane's part of a value row is contiguous too.
+template <int D, int RT>
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_f32(AttnArgs a, AttnSplit s) {
+    constexpr int KD = D / 4, NB = D / 16;
+    __shared__ AttnSchedLds sched;
+    __shared__ __align__(16) float join[4 * 16 * (D + 4)];
+    __shared__ float join_ml[4 * 16 * 2];
+    const AttnItem it0 = attn_item<false>(a, s, blockIdx.x, sched);
+    AttnItem it = it0;
+    it.found = uniform(it0.found);
+    if (!it.found) return;
+    it.req = uniform(it.req); it.h = uniform(it.h); it.tile = uniform(it.tile);
+    it.part = uniform(it.part); it.parts = uniform(it.parts); it.tiles = uniform(it.tiles);
+    it.row0 = uniform(it.row0); it.n = uniform(it.n); it.kept = uniform(it.kept);
+    it.C = uniform(it.C);
+    const int G = a.Hq / a.Hkv, wave = wave_id(), lane = threadIdx.x & 63;
+    const int c16 = lane & 15, g4 = lane >> 4;
+    const Keys keys = part_keys(a, s, it, G);
+    const int* table = a.table + (long)it.req * a.width;
+    const float scale = a.scale * kLog2e;
+    const int row_mask = (1 << a.page_shift) - 1;
+
+    f32x4 qf[RT][KD / 4];
+    int limit[RT];
+    for (int rt = 0; rt < RT; ++rt) {
+        const RowAt x = row_at(a, it, G, it.tile * s.R + rt * 16 + c16);
+        limit[rt] = x.in ? (int)min((long)it.kept + x.t, (long)kKeepAll) : -1;
+        const float* q = (const float*)a.q + x.q * D + g4 * KD;
+        for (int k = 0; k < KD / 4; ++k) {
+            f32x4 z = zero4();
+            if (x.in) z = *(const f32x4*)(q + 4 * k);
+            qf[rt][k] = z;
+        }
+    }
+    float m[RT], l[RT];
+    f32x4 acc[RT][NB];
+    for (int rt = 0; rt < RT; ++rt) {
+        m[rt] = -INFINITY;
+        l[rt] = 0.f;
+        for (int b = 0; b < NB; ++b) acc[rt][b] = zero4();
+    }
+
+    f32x4 kf[KD / 4];
+    float vf[4][NB];
+    auto base_of = [&](int p, int pos) {
+        return (((long)p * a.Hkv + it.h) << a.page_shift) + (pos & row_mask);
+    };
+    auto load_k = [&](int p, int pos) {
+        if (p >= 0) {
+            const float* k = (const float*)a.kc + (base_of(p, pos) + c16) * D + g4 * KD;
+            for (int i = 0; i < KD / 4; ++i) kf[i] = *(const f32x4*)(k + 4 * i);
+        } else {
+            for (int i = 0; i < KD / 4; ++i) kf[i] = zero4();
+        }
+    };
+    auto load_v = [&](int p, int pos) {
+        for (int i = 0; i < 4; ++i) {
+            const float* v = (const float*)a.vc + (base_of(p >= 0 ? p : 0, pos) + 4 * g4 + i) * D + c16 * NB;
+            for (int b = 0; b < NB; b += (NB < 4 ? NB : 4)) {
+                if (p < 0) {
+                    for (int j = 0; j < (NB < 4 ? NB : 4); ++j) vf[i][b + j] = 0.f;
+                } else if (NB >= 4) {
+                    const f32x4 x = *(const f32x4*)(v + b);
+                    for (int j = 0; j < 4; ++j) vf[i][b + j] = x[j];
+                } else {
+                    for (int j = 0; j < NB; ++j) vf[i][b + j] = v[b + j];
+                }
+            }
+        }
+    };
+
+    int pos = keys.begin + wave * 16;
+    int page = page_at(a, table, pos, keys.end);
+    if (pos < keys.end) {
+        load_k(page, pos);
+        load_v(page, pos);
+    }
+    for (; pos < keys.end; pos += 64) {
+        const int next = pos + 64;
+        const int page_next = page_at(a, table, next, keys.end);
+        f32x4 st[RT];
+        for (int rt = 0; rt < RT; ++rt) {
+            f32x4 x = zero4();
+            for (int k = 0; k < KD / 4; ++k)
+                for (int j = 0; j < 4; ++j) x = mma4(kf[k][j], qf[rt][k][j], x);
+            st[rt] = x;
+        }
+        if (next < keys.end) load_k(page_next, next);
+        float pe[RT][4];
+        for (int rt = 0; rt < RT; ++rt) {
+            float x[4];
+            for (int i = 0; i < 4; ++i) {
+                x[i] = st[rt][i] * scale;
+                const int key = pos + 4 * g4 + i;
+                if (key > limit[rt] || key >= keys.end || page < 0) x[i] = -INFINITY;
+            }
+            const float mx = max_quarters(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+            if (__any(mx > m[rt])) {
+                const float mn = fmaxf(m[rt], mx);
+                const float c = mn == -INFINITY ? 1.f : exp2_f(m[rt] - mn);
+                m[rt] = mn;
+                l[rt] *= c;
+                for (int b = 0; b < NB; ++b) acc[rt][b] *= c;
+            }
+            const float mu = m[rt] == -INFINITY ? 0.f : m[rt];
+            for (int i = 0; i < 4; ++i) {
+                pe[rt][i] = exp2_f(x[i] - mu);
+                l[rt] += pe[rt][i];
+            }
+        }
+        bool odd = false;
+        if (pos + 16 > keys.all) {
+            for (int i = 0; i < 4; ++i) {
+                const bool out = pos + 4 * g4 + i >= keys.end;
+                for (int b = 0; b < NB; ++b) {
+                    if (out) vf[i][b] = 0.f;         // no row sees it: it holds anything
+                    odd |= !finite_bits(vf[i][b]);
+                }
+            }
+            odd = __any(odd);
+        }
+        if (odd) {
+            // positions that only some rows see, with a value that is not
+            // finite: it must not meet the weight 0 of the other rows
+            for (int i = 0; i < 4; ++i)
+                for (int b = 0; b < NB; ++b)
+                    if (!finite_bits(vf[i][b])) vf[i][b] = 0.f;
+            for (int key = 0; key < 16; ++key) {
+                if (page < 0 || pos + key >= keys.end) continue;
+                const float* v = (const float*)a.vc + (base_of(page, pos) + key) * D;
+                for (int rt = 0; rt < RT; ++rt) {
+                    float w = 0.f;
+                    for (int i = 0; i < 4; ++i)
+                        if (i == (key & 3)) w = pe[rt][i];
+                    w = __shfl(w, c16 + 16 * (key / 4));
+                    const bool sees = pos + key <= limit[rt];
+                    for (int b = 0; b < NB; ++b)
+                        for (int i = 0; i < 4; ++i) {
+                            const float x = v[(4 * g4 + i) * NB + b];
+                            if (sees && !finite_bits(x)) acc[rt][b][i] += w * x;
+                        }
+                }
+            }
+        }
+        for (int i = 0; i < 4; ++i)
+            for (int b = 0; b < NB; ++b)
+                for (int rt = 0; rt < RT; ++rt) acc[rt][b] = mma4(vf[i][b], pe[rt][i], acc[rt][b]);
+        if (next < keys.end) load_v(page_next, next);
+        page = page_next;
+    }
+
+    for (int rt = 0; rt < RT; ++rt) {
+        const float sum = sum_quarters(l[rt]);
+        __syncthreads();
+        if (g4 == 0) {
+            join_ml[(wave * 16 + c16) * 2] = m[rt];
+            join_ml[(wave * 16 + c16) * 2 + 1] = sum;
+        }
+        for (int b = 0; b < NB; ++b)
+            for (int i = 0; i < 4; ++i)
+                join[(wave * 16 + c16) * (D + 4) + (4 * g4 + i) * NB + b] = acc[rt][b][i];
+        __syncthreads();
+        join_waves<float, D>(a, s, it, G, rt * 16, join_ml, join);
+    }
+}
+
+// Joins the parts of a tile that was cut: one workgroup per row, the four
+// waves over the parts in turn, the head over the lanes.
+template <typename T, int D>
+__global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit s) {
+    __shared__ AttnSchedLds sched;
+    __shared__ float part[4][D], part_l[4], red[4];
+    const AttnItem it = attn_item<true>(a, s, blockIdx.x / s.R, sched);
+    if (!it.found) return;
+    const int G = a.Hq / a.Hkv, row = blockIdx.x % s.R;
+    const RowAt x = row_at(a, it, G, it.tile * s.R + row);
+    if (!x.in) return;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const long step = (long)it.tiles * a.Hkv;
+    const long slot = it.slot + (long)it.tile * a.Hkv + it.h;
+    if (slot + step * (it.parts - 1) >= s.slots) return;
+    auto row_of = [&](int p) { return (slot + step * p) * s.R + row; };
+    float m = -INFINITY;
+    for (int p = tid; p < it.parts; p += kAttnThreads) m = fmaxf(m, s.ml[row_of(p) * 2]);
+    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if (lane == 0) red[w] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    constexpr int PER = D < 64 ? 1 : D / 64;
+    float l = 0.f, v[PER] = {};
+    for (int p = w; p < it.parts; p += 4) {
+        const float mp = s.ml[row_of(p) * 2], lp = s.ml[row_of(p) * 2 + 1];
+        if (lp == 0.f) continue;
+        const float c = mp == -INFINITY ? 1.f : exp2_f(mp - m);
+        l += c * lp;
+        if (lane * PER < D)
+            for (int i = 0; i < PER; ++i) v[i] += c * s.acc[row_of(p) * D + lane * PER + i];
+    }
+    if (lane * PER < D)
+        for (int i = 0; i < PER; ++i) part[w][lane * PER + i] = v[i];
+    if (lane == 0) part_l[w] = l;
+    __syncthreads();
+    l = part_l[0] + part_l[1] + part_l[2] + part_l[3];
+    if (tid < D) {
+        const float o = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
+        ((T*)a.o)[x.q * D + tid] = from_f32<T>(l == 0.f ? 0.f : o / l);
+    }
+    if (a.lse && tid == 0) a.lse[x.q] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+}
+
+// Kernels of a call, from sizes alone. Rows of a request are at most
+// max_new * G (T * G when the largest is not known).
+struct Plan {
+    AttnSplit split;
+    int RT;
+    long items, join_rows;
+    size_t bytes;
+};
+Plan plan_of(int T, int B, int Hq, int Hkv, int d, int max_new) {
+    const long G = Hq / Hkv, most = (max_new > 0 && max_new < T ? max_new : T) * G;
+    Plan p{};
+    p.RT = most <= 16 ? 1 : 2;
+    p.split.R = 16 * p.RT;
+    p.split.min_rows = 1;
+    p.split.max_rows = INT32_MAX;
+    p.split.unit = 128;
+    p.split.target_log2 = 11;
+    const long target = 1l << p.split.target_log2;
+    const long tiles = attn_max_tiles(T, B, G, Hkv, p.split.R);
+    p.items = attn_max_items(tiles, target);
+    p.split.slots = (int)attn_max_slots(target);
+    p.join_rows = (tiles < target ? tiles : target) * p.split.R;
+    p.bytes = (size_t)p.split.slots * p.split.R * (d + 2) * sizeof(float);
+    return p;
+}
+
+template <int D>
+hipError_t launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
+    const unsigned grid = (unsigned)p.items, rows = (unsigned)p.join_rows;
+    if (a.bf16_io) {
+        if (p.RT == 1) attn_stream_bf16<D, 1><<<grid, kAttnThreads, 0, st>>>(a, p.split);
+        else attn_stream_bf16<D, 2><<<grid, kAttnThreads, 0, st>>>(a, p.split);
+        attn_join<bf16, D><<<rows, kAttnThreads, 0, st>>>(a, p.split);
+    } else {
+        if (p.RT == 1) attn_stream_f32<D, 1><<<grid, kAttnThreads, 0, st>>>(a, p.split);
+        else attn_stream_f32<D, 2><<<grid, kAttnThreads, 0, st>>>(a, p.split);
+        attn_join<float, D><<<rows, kAttnThreads, 0, st>>>(a, p.split);
+    }
+    return hipGetLastError();
 }
 
 }  // namespace
 
-size_t attn_paged_ws(int, int, int, int, int, int, bool) { return 0; }
+size_t attn_paged_ws(int T, int B, int Hq, int Hkv, int d, int max_new, bool) {
+    return plan_of(T, B, Hq, Hkv, d, max_new).bytes;
+}
 
-hipError_t launch_attn_paged(const AttnArgs& a, void*, hipStream_t st) {
-    if (a.bf16_io) launch<bf16>(a, st);
-    else launch<float>(a, st);
-    return hipGetLastError();
+hipError_t launch_attn_paged(const AttnArgs& a, void* ws, hipStream_t st) {
+    Plan p = plan_of(a.T, a.B, a.Hq, a.Hkv, a.d, a.max_new);
+    p.split.ml = (float*)ws;
+    p.split.acc = p.split.ml + (size_t)p.split.slots * p.split.R * 2;
+    switch (a.d) {
+        case 16: return launch<16>(a, p, st);
+        case 32: return launch<32>(a, p, st);
+        case 64: return launch<64>(a, p, st);
+        default: return launch<128>(a, p, st);
+    }
 }
 
 }  // namespace kda

@@ -12,6 +12,7 @@
 namespace {
 
 constexpr size_t kMaxBytes = SIZE_MAX >> 3;
+constexpr size_t kMaxRows = (size_t)1 << 30;   // query rows, positions: 32-bit indices with room
 
 bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 bool page_ok(int p) { return p >= 16 && p <= 1024 && (p & (p - 1)) == 0; }
@@ -129,7 +130,7 @@ size_t kda_attn_paged_workspace_size(int T, int B, int Hq, int Hkv, int d, int m
                                      kda_dtype dtype) {
     if (T <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || !dim_ok(d) || max_new < 0) return 0;
     if (dtype != KDA_F32 && dtype != KDA_BF16) return 0;
-    if (product(T, Hq, d, 4) > kMaxBytes || product(T, Hq) > INT32_MAX) return 0;
+    if (product(T, Hq, d, 4) > kMaxBytes || product(T, Hq) > kMaxRows) return 0;
     return kda::attn_paged_ws(T, B, Hq, Hkv, d, max_new, dtype == KDA_BF16);
 }
 
@@ -149,9 +150,8 @@ kda_status kda_attn_paged(const void* q, const void* k_cache, const void* v_cach
     const size_t elt = dtype == KDA_BF16 ? 2 : 4;
     const size_t rows = product(T, Hq, d, elt), cache = product(n_pool, Hkv, page_size, d, elt);
     const size_t table = product(B, max_pages, 4);
-    // query rows are numbered in 32 bits
     if (rows > kMaxBytes || cache > kMaxBytes || table > kMaxBytes ||
-        product(T, Hq) > INT32_MAX || (long)max_pages * page_size > INT32_MAX)
+        product(T, Hq) > kMaxRows || product(max_pages, page_size) > kMaxRows)
         return KDA_ERR_INVALID_ARG;
     if (!q || !o || !kept_len || !cu_new || (table && !block_table) ||
         (cache && (!k_cache || !v_cache)))

@@ -108,6 +108,7 @@ kda_status kda_cache_append(const void* k, const void* v, const int* slot_map,
  *   lse      [T, Hq] fp32 or NULL: natural log of the sum of exp(scores),
  *            -infinity for a row without any position
  *   scale    factor on q.k; 0 selects 1 / sqrt(d). Finite, not negative.
+ *            T * Hq and max_pages * page_size are at most 2^30.
  *   max_new  the largest number of new tokens of one request, 0 = unknown. It
  *            selects kernels only: results are right whatever it says.
  *   ws       kda_attn_paged_workspace_size() bytes

@@ -20,6 +20,10 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 constexpr int kKeepAll = 1 << 30;
+#ifndef KTG
+#define KTG 1
+#endif
+constexpr int kTileGroups = KTG;
 
 __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -120,10 +124,17 @@ __device__ __forceinline__ Keys part_keys(const AttnArgs& a, const AttnSplit& s,
     return k;
 }
 
+// A request's row of the block table. Nothing writes it while the kernel runs,
+// so its entries are read as constants: scalar loads, which do not wait for
+// the keys and values in flight as vector loads would.
+typedef const __attribute__((address_space(4))) int const_int;
+__device__ __forceinline__ const_int* table_row(const AttnArgs& a, int req) {
+    return (const_int*)(uintptr_t)(a.table + (long)req * a.width);
+}
 // Page id of the 16 positions at pos (a multiple of 16), -1 when there is none.
-__device__ __forceinline__ int page_at(const AttnArgs& a, const int* table, int pos, int end) {
+__device__ __forceinline__ int page_at(const AttnArgs& a, const_int* table, int pos, int end) {
     if (pos >= end) return -1;
-    const int p = uniform(table[pos >> a.page_shift]);
+    const int p = table[pos >> a.page_shift];
     return (unsigned)p < (unsigned)a.pool ? p : -1;
 }
 
@@ -156,7 +167,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, 
     const int G = a.Hq / a.Hkv, wave = wave_id(), lane = threadIdx.x & 63;
     const int c16 = lane & 15, g4 = lane >> 4;
     const Keys keys = part_keys(a, s, it, G);
-    const int* table = a.table + (long)it.req * a.width;
+    const_int* table = table_row(a, it.req);
     const float scale = a.scale * kLog2e;
     bf16* stage = (bf16*)join + wave * (32 * D);     // V of this wave's 32 keys
 
@@ -381,7 +392,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_f32(AttnArgs a, A
     const int G = a.Hq / a.Hkv, wave = wave_id(), lane = threadIdx.x & 63;
     const int c16 = lane & 15, g4 = lane >> 4;
     const Keys keys = part_keys(a, s, it, G);
-    const int* table = a.table + (long)it.req * a.width;
+    const_int* table = table_row(a, it.req);
     const float scale = a.scale * kLog2e;
     const int row_mask = (1 << a.page_shift) - 1;
 
@@ -529,101 +540,393 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_f32(AttnArgs a, A
     }
 }
 
-// Joins the parts of a tile that was cut: one workgroup per row, the four
-// waves over the parts in turn, the head over the lanes.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void glb_void;
+
+// D(32x32) += A(32x16) B(16x32): lane l holds A[l%32][8(l/32)..+7],
+// B[8(l/32)..+7][l%32], D[8(i/4) + 4(l/32) + i%4][l%32] in element i.
+__device__ __forceinline__ f32x16 mma_big(bf16x8 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ float max_halves(float x) { return fmaxf(x, __shfl_xor(x, 32)); }
+
+// Prompts: tiles of 128 RW rows, 32 RW per wave, against 64 keys at a time
+// that all waves share in LDS, double buffered. What bounds it is the matrix
+// cores, 4 D flops per row and key, and next to them the exponentials.
+//
+// As above S^T = K Q^T and O^T += V^T P^T, with the 32x32x16 product: the
+// scores of row l % 32 stay in lanes l and l + 32 and are the second operand
+// of the next product as they are. K and V go from memory to LDS directly, 16
+// bytes a lane in the lanes' order; which 16 bytes of the row each lane
+// fetches is permuted, so that the reads meet no bank twice: K's pieces by
+// the key's low 3 bits (8 lanes read the same piece of 8 keys), V's pairs of
+// pieces by its low 2 (a 16-lane transposing read takes 32 bytes of 4 keys).
+template <int D, int RW>
+__global__ __launch_bounds__(kAttnThreads, RW == 1 ? 2 : 1) void attn_tile_bf16(AttnArgs a,
+                                                                               AttnSplit s) {
+    constexpr int KS = D / 16, NB = D / 32, CH = D / 8, LD = 16 * CH / 64;
+    __shared__ AttnSchedLds sched;
+    __shared__ __align__(128) bf16 kbuf[2][64 * D], vbuf[2][64 * D];
+    __shared__ int gap_wave[2][4], odd_wave[4];
+    AttnItem it = attn_item<false>(a, s, blockIdx.x, sched);
+    it.found = uniform(it.found);
+    if (!it.found) return;
+    it.req = uniform(it.req); it.h = uniform(it.h); it.tile = uniform(it.tile);
+    it.part = uniform(it.part); it.parts = uniform(it.parts); it.tiles = uniform(it.tiles);
+    it.row0 = uniform(it.row0); it.n = uniform(it.n); it.kept = uniform(it.kept);
+    it.C = uniform(it.C);
+    const int G = a.Hq / a.Hkv, wave = wave_id(), lane = threadIdx.x & 63;
+    const int c32 = lane & 31, half = lane >> 5;
+    const Keys keys = part_keys(a, s, it, G);
+    const_int* table = table_row(a, it.req);
+    const float scale = a.scale * kLog2e;
+    const int row_mask = (1 << a.page_shift) - 1;
+
+    bf16x8 qf[RW][KS];
+    int limit[RW];
+    RowAt at[RW];
+    for (int rw = 0; rw < RW; ++rw) {
+        at[rw] = row_at(a, it, G, it.tile * s.R + (wave * RW + rw) * 32 + c32);
+        limit[rw] = at[rw].in ? (int)min((long)it.kept + at[rw].t, (long)kKeepAll) : -1;
+        const bf16* q = (const bf16*)a.q + at[rw].q * D + 8 * half;
+        for (int k = 0; k < KS; ++k) {
+            bf16x8 z = {};
+            if (at[rw].in) z = *(const bf16x8*)(q + 16 * k);
+            qf[rw][k] = z;
+        }
+    }
+    float m[RW], l[RW];
+    f32x16 acc[RW][NB];
+    for (int rw = 0; rw < RW; ++rw) {
+        m[rw] = -INFINITY;
+        l[rw] = 0.f;
+        for (int b = 0; b < NB; ++b) acc[rw][b] = f32x16{};
+    }
+
+    // This wave's 16 keys of the tile at pos, from page p (-1: zeros).
+    auto fetch = [&](int buf, int pos, int p) {
+        bf16* k = kbuf[buf] + 16 * wave * D;
+        bf16* v = vbuf[buf] + 16 * wave * D;
+        if (p >= 0) {
+            const long row = (((long)p * a.Hkv + it.h) << a.page_shift) + ((pos + 16 * wave) & row_mask);
+            const bf16* gk = (const bf16*)a.kc + row * D;
+            const bf16* gv = (const bf16*)a.vc + row * D;
+            for (int i = 0; i < LD; ++i) {
+                const int x = i * 64 + lane, r = x / CH, c = x % CH;
+                __builtin_amdgcn_global_load_lds((glb_void*)(gk + r * D + 8 * (c ^ (r & 7))),
+                                                 (lds_void*)(k + i * 512), 16, 0, 0);
+                __builtin_amdgcn_global_load_lds((glb_void*)(gv + r * D + 8 * (c ^ (2 * (r & 3)))),
+                                                 (lds_void*)(v + i * 512), 16, 0, 0);
+            }
+        } else {
+            for (int i = 0; i < LD; ++i) {
+                *(bf16x8*)(k + i * 512 + 8 * lane) = bf16x8{};
+                *(bf16x8*)(v + i * 512 + 8 * lane) = bf16x8{};
+            }
+        }
+    };
+    auto page_of = [&](int pos) { return page_at(a, table, pos + 16 * wave, keys.end); };
+
+    int buf = 0, page = page_of(keys.begin), page_next = page_of(keys.begin + 64);
+    if (keys.begin < keys.end) fetch(0, keys.begin, page);
+    for (int pos = keys.begin; pos < keys.end; pos += 64, buf ^= 1) {
+        // missing pages are known to the wave that fetches them only; two sets
+        // of flags, since a wave may set the next ones while another reads these
+        if (lane == 0) gap_wave[buf][wave] = page < 0;
+        __builtin_amdgcn_s_waitcnt(0x0f70);          // vmcnt(0): this wave's part has landed
+        __syncthreads();
+        int missing = 0;
+        for (int w = 0; w < 4; ++w) missing |= uniform(gap_wave[buf][w]) << w;
+        const bool edge = pos + 64 > keys.all || missing;
+        const bf16* kt = kbuf[buf];
+        bf16* vt = vbuf[buf];
+        page = page_next;
+        page_next = page_of(pos + 128);
+        if (pos + 64 < keys.end) fetch(buf ^ 1, pos + 64, page);
+        bool odd = false;
+        if (edge) {
+            // rows that no row of the tile sees hold anything: they count 0
+            for (int i = 0; i < LD; ++i) {
+                bf16* v = vt + (16 * wave) * D + i * 512 + 8 * lane;
+                if (pos + 16 * wave + (i * 64 + lane) / CH >= keys.end) *(bf16x8*)v = bf16x8{};
+                const bf16x8 x = *(const bf16x8*)v;
+                for (int j = 0; j < 8; ++j) odd |= !finite_bits((float)x[j]);
+            }
+            if (lane == 0) odd_wave[wave] = 0;
+            if (__any(odd) && lane == 0) odd_wave[wave] = 1;
+            __syncthreads();                         // the rows are cleared, the flags set
+            odd = uniform(odd_wave[0] | odd_wave[1] | odd_wave[2] | odd_wave[3]);
+            __syncthreads();                         // and read
+        }
+
+        f32x16 st[RW][2];
+        for (int u = 0; u < 2; ++u) {
+            for (int rw = 0; rw < RW; ++rw) st[rw][u] = f32x16{};
+            for (int k = 0; k < KS; ++k) {
+                const int c = (2 * k + half) ^ (c32 & 7);
+                const bf16x8 kf = *(const bf16x8*)(kt + (32 * u + c32) * D + 8 * c);
+                for (int rw = 0; rw < RW; ++rw) st[rw][u] = mma_big(kf, qf[rw][k], st[rw][u]);
+            }
+        }
+        bf16x8 pf[RW][4];
+        for (int rw = 0; rw < RW; ++rw) {
+            if (edge) {
+                for (int u = 0; u < 2; ++u)
+                    for (int i = 0; i < 16; ++i) {
+                        const int y = 32 * u + 8 * (i / 4) + 4 * half + i % 4;
+                        if (pos + y > limit[rw] || pos + y >= keys.end || (missing >> (y / 16) & 1))
+                            st[rw][u][i] = -INFINITY;
+                    }
+            }
+            float mx = -INFINITY;
+            for (int u = 0; u < 2; ++u)
+                for (int i = 0; i < 16; ++i) mx = fmaxf(mx, st[rw][u][i]);
+            mx = max_halves(mx) * scale;
+            // The reference m may stay behind the maximum by up to 8 in the
+            // log2 domain: weights up to 2^8 lose nothing, and the rows are
+            // rescaled a few times instead of with every new maximum.
+            if (__any(mx > m[rw] + 8.f)) {
+                const float mn = fmaxf(m[rw], mx);
+                const float c = mn == -INFINITY ? 1.f : exp2_f(m[rw] - mn);
+                m[rw] = mn;
+                l[rw] *= c;
+                for (int b = 0; b < NB; ++b) acc[rw][b] *= c;
+            }
+            const float mu = m[rw] == -INFINITY ? 0.f : m[rw];
+            float sum = 0.f;
+            for (int u = 0; u < 2; ++u)
+                for (int i = 0; i < 16; ++i) {
+                    const float p = exp2_f(__builtin_fmaf(st[rw][u][i], scale, -mu));
+                    sum += p;
+                    st[rw][u][i] = p;
+                }
+            l[rw] += sum;
+            for (int ks = 0; ks < 4; ++ks)
+                for (int j = 0; j < 8; ++j) pf[rw][ks][j] = (bf16)st[rw][ks / 2][8 * (ks % 2) + j];
+        }
+        for (int ks = 0; ks < 4; ++ks)
+            for (int b = 0; b < NB; ++b) {
+                s16x4 x[2];
+                for (int j = 0; j < 2; ++j) {
+                    const int key = 16 * ks + 8 * j + 4 * half + (lane & 15) / 4;
+                    const int dv = 32 * b + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+                    const int c = (dv / 8) ^ (2 * (key & 3));
+                    x[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (lds_s16x4*)(vt + key * D + 8 * c + dv % 8));
+                }
+                bf16x8 va = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                if (odd)
+                    for (int j = 0; j < 8; ++j)
+                        if (!finite_bits((float)va[j])) va[j] = (bf16)0.f;
+                for (int rw = 0; rw < RW; ++rw) acc[rw][b] = mma_big(va, pf[rw][ks], acc[rw][b]);
+            }
+        if (odd) {
+            // the values left out above, for the rows that see them
+            for (int y = 0; y < 64; ++y) {
+                if (pos + y >= keys.end || (missing >> (y / 16) & 1)) continue;
+                for (int rw = 0; rw < RW; ++rw) {
+                    float w = 0.f;
+                    for (int u = 0; u < 2; ++u)
+                        for (int i = 0; i < 16; ++i)
+                            if (y / 32 == u && (y & 31) / 8 == i / 4 && y % 4 == i % 4) w = st[rw][u][i];
+                    w = __shfl(w, c32 + 32 * ((y / 4) & 1));
+                    const bool sees = pos + y <= limit[rw];
+                    for (int b = 0; b < NB; ++b)
+                        for (int i = 0; i < 16; ++i) {
+                            const int dv = 32 * b + 8 * (i / 4) + 4 * half + i % 4;
+                            const float v = (float)vt[y * D + 8 * ((dv / 8) ^ (2 * (y & 3))) + dv % 8];
+                            if (sees && !finite_bits(v)) acc[rw][b][i] += w * v;
+                        }
+                }
+            }
+        }
+    }
+
+    for (int rw = 0; rw < RW; ++rw) {
+        const float sum = l[rw] + __shfl_xor(l[rw], 32);
+        const int row = (wave * RW + rw) * 32 + c32;
+        if (it.parts > 1) {
+            const long slot = it.slot + ((long)it.part * it.tiles + it.tile) * a.Hkv + it.h;
+            if (slot >= s.slots) return;
+            float* x = s.acc + (slot * s.R + row) * D;
+            for (int b = 0; b < NB; ++b)
+                for (int i = 0; i < 16; i += 4)
+                    *(f32x4*)(x + 32 * b + 2 * i + 4 * half) =
+                        f32x4{acc[rw][b][i], acc[rw][b][i + 1], acc[rw][b][i + 2], acc[rw][b][i + 3]};
+            if (half == 0) {
+                s.ml[(slot * s.R + row) * 2] = m[rw];
+                s.ml[(slot * s.R + row) * 2 + 1] = sum;
+            }
+            continue;
+        }
+        if (!at[rw].in) continue;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        bf16* o = (bf16*)a.o + at[rw].q * D;
+        for (int b = 0; b < NB; ++b)
+            for (int i = 0; i < 16; i += 4) {
+                bf16x4 x;
+                for (int j = 0; j < 4; ++j) x[j] = (bf16)(acc[rw][b][i + j] * inv);
+                *(bf16x4*)(o + 32 * b + 2 * i + 4 * half) = x;
+            }
+        if (a.lse && half == 0) a.lse[at[rw].q] = sum == 0.f ? -INFINITY : (m[rw] + __log2f(sum)) * kLn2;
+    }
+}
+
+// Joins the parts of tiles that were cut: `per` rows of one tile a workgroup,
+// for each row the four waves over the parts in turn, the head over the lanes.
 template <typename T, int D>
-__global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit s) {
+__global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit s, int per) {
     __shared__ AttnSchedLds sched;
     __shared__ float part[4][D], part_l[4], red[4];
-    const AttnItem it = attn_item<true>(a, s, blockIdx.x / s.R, sched);
+    const unsigned per_tile = (unsigned)(s.R / per);
+    const AttnItem it = attn_item<true>(a, s, blockIdx.x / per_tile, sched);
     if (!it.found) return;
-    const int G = a.Hq / a.Hkv, row = blockIdx.x % s.R;
-    const RowAt x = row_at(a, it, G, it.tile * s.R + row);
-    if (!x.in) return;
+    const int G = a.Hq / a.Hkv, row0 = (int)(blockIdx.x % per_tile) * per;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const long step = (long)it.tiles * a.Hkv;
     const long slot = it.slot + (long)it.tile * a.Hkv + it.h;
     if (slot + step * (it.parts - 1) >= s.slots) return;
-    auto row_of = [&](int p) { return (slot + step * p) * s.R + row; };
-    float m = -INFINITY;
-    for (int p = tid; p < it.parts; p += kAttnThreads) m = fmaxf(m, s.ml[row_of(p) * 2]);
-    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    if (lane == 0) red[w] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
     constexpr int PER = D < 64 ? 1 : D / 64;
-    float l = 0.f, v[PER] = {};
-    for (int p = w; p < it.parts; p += 4) {
-        const float mp = s.ml[row_of(p) * 2], lp = s.ml[row_of(p) * 2 + 1];
-        if (lp == 0.f) continue;
-        const float c = mp == -INFINITY ? 1.f : exp2_f(mp - m);
-        l += c * lp;
+    for (int row = row0; row < row0 + per; ++row) {
+        const RowAt x = row_at(a, it, G, it.tile * s.R + row);
+        if (!x.in) return;
+        auto row_of = [&](int p) { return (slot + step * p) * s.R + row; };
+        float m = -INFINITY;
+        for (int p = tid; p < it.parts; p += kAttnThreads) m = fmaxf(m, s.ml[row_of(p) * 2]);
+        for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+        if (lane == 0) red[w] = m;
+        __syncthreads();
+        m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        float l = 0.f, v[PER] = {};
+        for (int p = w; p < it.parts; p += 4) {
+            const float mp = s.ml[row_of(p) * 2], lp = s.ml[row_of(p) * 2 + 1];
+            if (lp == 0.f) continue;                 // a part without a key of this row
+            const float c = mp == -INFINITY ? 1.f : exp2_f(mp - m);
+            l += c * lp;
+            if (lane * PER < D)
+                for (int i = 0; i < PER; ++i) v[i] += c * s.acc[row_of(p) * D + lane * PER + i];
+        }
         if (lane * PER < D)
-            for (int i = 0; i < PER; ++i) v[i] += c * s.acc[row_of(p) * D + lane * PER + i];
+            for (int i = 0; i < PER; ++i) part[w][lane * PER + i] = v[i];
+        if (lane == 0) part_l[w] = l;
+        __syncthreads();
+        l = part_l[0] + part_l[1] + part_l[2] + part_l[3];
+        if (tid < D) {
+            const float o = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
+            ((T*)a.o)[x.q * D + tid] = from_f32<T>(l == 0.f ? 0.f : o / l);
+        }
+        if (a.lse && tid == 0) a.lse[x.q] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+        __syncthreads();                             // part, part_l and red are free again
     }
-    if (lane * PER < D)
-        for (int i = 0; i < PER; ++i) part[w][lane * PER + i] = v[i];
-    if (lane == 0) part_l[w] = l;
-    __syncthreads();
-    l = part_l[0] + part_l[1] + part_l[2] + part_l[3];
-    if (tid < D) {
-        const float o = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
-        ((T*)a.o)[x.q * D + tid] = from_f32<T>(l == 0.f ? 0.f : o / l);
-    }
-    if (a.lse && tid == 0) a.lse[x.q] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
 // Kernels of a call, from sizes alone. Rows of a request are at most
 // max_new * G (T * G when the largest is not known).
-struct Plan {
+//
+// Up to kStreamRows rows a request is the stream kernels'; of a call with
+// larger ones (bf16, d of 64 and 128) those go to the tile kernel, and the
+// rest to a second launch.
+constexpr int kStreamRows = 32;
+
+struct Launch {
     AttnSplit split;
-    int RT;
-    long items, join_rows;
-    size_t bytes;
+    long items, joins;     // workgroups
+    int per;               // rows a joining workgroup takes
 };
-Plan plan_of(int T, int B, int Hq, int Hkv, int d, int max_new) {
+struct Plan {
+    int n;                 // launches
+    bool tiles;            // the first is the tile kernel
+    int RT;                // row groups of the stream kernel
+    Launch l[2];
+    size_t bytes;          // workspace: the launches use it in turn
+};
+Launch launch_of(long T, long B, long G, long Hkv, int R, int unit, int target_log2) {
+    Launch l{};
+    l.split.R = R;
+    l.split.min_rows = 1;
+    l.split.max_rows = INT32_MAX;
+    l.split.unit = unit;
+    l.split.target_log2 = target_log2;
+    const long target = 1l << target_log2, tiles = attn_max_tiles(T, B, G, Hkv, R);
+    l.items = attn_max_items(tiles, target);
+    l.split.slots = (int)attn_max_slots(target);
+    // about 1024 workgroups for the joining: with fewer rows they take one each
+    const long rows = (tiles < target ? tiles : target) * R;
+    l.per = 1;
+    while (l.per < R && rows / l.per > 1024) l.per *= 2;
+    l.joins = rows / l.per;
+    return l;
+}
+Plan plan_of(int T, int B, int Hq, int Hkv, int d, int max_new, bool bf16_io) {
     const long G = Hq / Hkv, most = (max_new > 0 && max_new < T ? max_new : T) * G;
     Plan p{};
+    p.tiles = bf16_io && d >= 64 && most > kStreamRows;
     p.RT = most <= 16 ? 1 : 2;
-    p.split.R = 16 * p.RT;
-    p.split.min_rows = 1;
-    p.split.max_rows = INT32_MAX;
-    p.split.unit = 128;
-    p.split.target_log2 = 11;
-    const long target = 1l << p.split.target_log2;
-    const long tiles = attn_max_tiles(T, B, G, Hkv, p.split.R);
-    p.items = attn_max_items(tiles, target);
-    p.split.slots = (int)attn_max_slots(target);
-    p.join_rows = (tiles < target ? tiles : target) * p.split.R;
-    p.bytes = (size_t)p.split.slots * p.split.R * (d + 2) * sizeof(float);
+    if (p.tiles) {
+        p.l[p.n] = launch_of(T, B, G, Hkv, 128 * kTileGroups, 64, 9);
+        p.l[p.n].split.min_rows = kStreamRows + 1;
+        ++p.n;
+    }
+    if (!p.tiles || B > 1) {
+        p.l[p.n] = launch_of(T, B, G, Hkv, 16 * p.RT, 128, 11);
+        if (p.tiles) p.l[p.n].split.max_rows = kStreamRows;
+        ++p.n;
+    }
+    // a single request is the tile kernel's whatever its length
+    if (p.tiles && B == 1) p.l[0].split.min_rows = 1;
+    for (int i = 0; i < p.n; ++i) {
+        const size_t x = (size_t)p.l[i].split.slots * p.l[i].split.R * (d + 2) * sizeof(float);
+        if (x > p.bytes) p.bytes = x;
+    }
     return p;
 }
 
 template <int D>
-hipError_t launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
-    const unsigned grid = (unsigned)p.items, rows = (unsigned)p.join_rows;
+void launch_stream(const AttnArgs& a, const Plan& p, const Launch& l, hipStream_t st) {
+    const unsigned grid = (unsigned)l.items;
     if (a.bf16_io) {
-        if (p.RT == 1) attn_stream_bf16<D, 1><<<grid, kAttnThreads, 0, st>>>(a, p.split);
-        else attn_stream_bf16<D, 2><<<grid, kAttnThreads, 0, st>>>(a, p.split);
-        attn_join<bf16, D><<<rows, kAttnThreads, 0, st>>>(a, p.split);
+        if (p.RT == 1) attn_stream_bf16<D, 1><<<grid, kAttnThreads, 0, st>>>(a, l.split);
+        else attn_stream_bf16<D, 2><<<grid, kAttnThreads, 0, st>>>(a, l.split);
     } else {
-        if (p.RT == 1) attn_stream_f32<D, 1><<<grid, kAttnThreads, 0, st>>>(a, p.split);
-        else attn_stream_f32<D, 2><<<grid, kAttnThreads, 0, st>>>(a, p.split);
-        attn_join<float, D><<<rows, kAttnThreads, 0, st>>>(a, p.split);
+        if (p.RT == 1) attn_stream_f32<D, 1><<<grid, kAttnThreads, 0, st>>>(a, l.split);
+        else attn_stream_f32<D, 2><<<grid, kAttnThreads, 0, st>>>(a, l.split);
+    }
+}
+template <int D>
+void launch_tile(const AttnArgs& a, const Launch& l, hipStream_t st) {
+    attn_tile_bf16<D, kTileGroups><<<(unsigned)l.items, kAttnThreads, 0, st>>>(a, l.split);
+}
+
+template <int D>
+hipError_t launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
+    for (int i = 0; i < p.n; ++i) {
+        const Launch& l = p.l[i];
+        if (i == 0 && p.tiles) {
+            if constexpr (D >= 64) launch_tile<D>(a, l, st);
+        } else {
+            launch_stream<D>(a, p, l, st);
+        }
+        const unsigned n = (unsigned)l.joins;
+        if (a.bf16_io) attn_join<bf16, D><<<n, kAttnThreads, 0, st>>>(a, l.split, l.per);
+        else attn_join<float, D><<<n, kAttnThreads, 0, st>>>(a, l.split, l.per);
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t attn_paged_ws(int T, int B, int Hq, int Hkv, int d, int max_new, bool) {
-    return plan_of(T, B, Hq, Hkv, d, max_new).bytes;
+size_t attn_paged_ws(int T, int B, int Hq, int Hkv, int d, int max_new, bool bf16_io) {
+    return plan_of(T, B, Hq, Hkv, d, max_new, bf16_io).bytes;
 }
 
 hipError_t launch_attn_paged(const AttnArgs& a, void* ws, hipStream_t st) {
-    Plan p = plan_of(a.T, a.B, a.Hq, a.Hkv, a.d, a.max_new);
-    p.split.ml = (float*)ws;
-    p.split.acc = p.split.ml + (size_t)p.split.slots * p.split.R * 2;
+    Plan p = plan_of(a.T, a.B, a.Hq, a.Hkv, a.d, a.max_new, a.bf16_io);
+    for (int i = 0; i < p.n; ++i) {
+        AttnSplit& s = p.l[i].split;
+        s.ml = (float*)ws;
+        s.acc = s.ml + (size_t)s.slots * s.R * 2;
+    }
     switch (a.d) {
         case 16: return launch<16>(a, p, st);
         case 32: return launch<32>(a, p, st);

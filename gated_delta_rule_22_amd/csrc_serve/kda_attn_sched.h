@@ -113,7 +113,8 @@ __device__ __forceinline__ AttnItem attn_item(const AttnArgs& a, const AttnSplit
             AttnItem it;
             it.req = base + tid;
             it.h = (int)(local % (unsigned)a.Hkv);
-            it.tile = (int)(rest % (unsigned)r.tiles);
+            // the last tile first: it sees the most keys
+            it.tile = r.tiles - 1 - (int)(rest % (unsigned)r.tiles);
             it.part = (int)(rest / (unsigned)r.tiles);
             it.parts = (int)parts;
             it.tiles = r.tiles;

@@ -93,8 +93,8 @@ __device__ __forceinline__ void join_waves(const AttnArgs& a, const AttnSplit& s
     }
     const int r = it.tile * s.R + r0 + row;
     if (it.parts > 1) {
-        const long slot = it.slot + ((long)it.part * it.tiles + it.tile) * a.Hkv + it.h;
-        if (slot >= s.slots) return;                // offsets that decrease: see attn_req
+        const long slot = (long)it.slot + ((long)it.part * it.tiles + it.tile) * a.Hkv + it.h;
+        if ((unsigned long)slot >= (unsigned long)s.slots) return;   // only where offsets decrease
         const long at = slot * s.R + r0 + row;
         for (int i = 0; i < kPer; i += 4)
             *(f32x4*)(s.acc + at * D + d + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
@@ -152,18 +152,12 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, 
     constexpr int NB = D / 16;                       // value columns in 16s
     constexpr int VL = D / 16;                       // 16-byte loads per lane for 32 rows of V
     constexpr int CH = D / 8;                        // 16-byte pieces of a row
-    __shared__ AttnSchedLds sched;
     __shared__ __align__(16) float join[4 * 16 * (D + 4) > 4 * 32 * D / 2 ? 4 * 16 * (D + 4)
                                                                          : 4 * 32 * D / 2];
     __shared__ float join_ml[4 * 16 * 2];
-    const AttnItem it0 = attn_item<false>(a, s, blockIdx.x, sched);
-    AttnItem it = it0;
-    it.found = uniform(it0.found);
+    __shared__ AttnItem shared_item;
+    const AttnItem it = attn_item(a, s, (int)blockIdx.x, shared_item);
     if (!it.found) return;
-    it.req = uniform(it.req); it.h = uniform(it.h); it.tile = uniform(it.tile);
-    it.part = uniform(it.part); it.parts = uniform(it.parts); it.tiles = uniform(it.tiles);
-    it.row0 = uniform(it.row0); it.n = uniform(it.n); it.kept = uniform(it.kept);
-    it.C = uniform(it.C);
     const int G = a.Hq / a.Hkv, wave = wave_id(), lane = threadIdx.x & 63;
     const int c16 = lane & 15, g4 = lane >> 4;
     const Keys keys = part_keys(a, s, it, G);
@@ -378,17 +372,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, 
 template <int D, int RT>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_f32(AttnArgs a, AttnSplit s) {
     constexpr int KD = D / 4, NB = D / 16;
-    __shared__ AttnSchedLds sched;
     __shared__ __align__(16) float join[4 * 16 * (D + 4)];
     __shared__ float join_ml[4 * 16 * 2];
-    const AttnItem it0 = attn_item<false>(a, s, blockIdx.x, sched);
-    AttnItem it = it0;
-    it.found = uniform(it0.found);
+    __shared__ AttnItem shared_item;
+    const AttnItem it = attn_item(a, s, (int)blockIdx.x, shared_item);
     if (!it.found) return;
-    it.req = uniform(it.req); it.h = uniform(it.h); it.tile = uniform(it.tile);
-    it.part = uniform(it.part); it.parts = uniform(it.parts); it.tiles = uniform(it.tiles);
-    it.row0 = uniform(it.row0); it.n = uniform(it.n); it.kept = uniform(it.kept);
-    it.C = uniform(it.C);
     const int G = a.Hq / a.Hkv, wave = wave_id(), lane = threadIdx.x & 63;
     const int c16 = lane & 15, g4 = lane >> 4;
     const Keys keys = part_keys(a, s, it, G);
@@ -566,16 +554,11 @@ template <int D, int RW>
 __global__ __launch_bounds__(kAttnThreads, RW == 1 ? 2 : 1) void attn_tile_bf16(AttnArgs a,
                                                                                AttnSplit s) {
     constexpr int KS = D / 16, NB = D / 32, CH = D / 8, LD = 16 * CH / 64;
-    __shared__ AttnSchedLds sched;
     __shared__ __align__(128) bf16 kbuf[2][64 * D], vbuf[2][64 * D];
     __shared__ int gap_wave[2][4], odd_wave[4];
-    AttnItem it = attn_item<false>(a, s, blockIdx.x, sched);
-    it.found = uniform(it.found);
+    __shared__ AttnItem shared_item;
+    const AttnItem it = attn_item(a, s, (int)blockIdx.x, shared_item);
     if (!it.found) return;
-    it.req = uniform(it.req); it.h = uniform(it.h); it.tile = uniform(it.tile);
-    it.part = uniform(it.part); it.parts = uniform(it.parts); it.tiles = uniform(it.tiles);
-    it.row0 = uniform(it.row0); it.n = uniform(it.n); it.kept = uniform(it.kept);
-    it.C = uniform(it.C);
     const int G = a.Hq / a.Hkv, wave = wave_id(), lane = threadIdx.x & 63;
     const int c32 = lane & 31, half = lane >> 5;
     const Keys keys = part_keys(a, s, it, G);
@@ -747,8 +730,8 @@ __global__ __launch_bounds__(kAttnThreads, RW == 1 ? 2 : 1) void attn_tile_bf16(
         const float sum = l[rw] + __shfl_xor(l[rw], 32);
         const int row = (wave * RW + rw) * 32 + c32;
         if (it.parts > 1) {
-            const long slot = it.slot + ((long)it.part * it.tiles + it.tile) * a.Hkv + it.h;
-            if (slot >= s.slots) return;
+            const long slot = (long)it.slot + ((long)it.part * it.tiles + it.tile) * a.Hkv + it.h;
+            if ((unsigned long)slot >= (unsigned long)s.slots) return;
             float* x = s.acc + (slot * s.R + row) * D;
             for (int b = 0; b < NB; ++b)
                 for (int i = 0; i < 16; i += 4)
@@ -773,51 +756,103 @@ __global__ __launch_bounds__(kAttnThreads, RW == 1 ? 2 : 1) void attn_tile_bf16(
     }
 }
 
-// Joins the parts of tiles that were cut: `per` rows of one tile a workgroup,
-// for each row the four waves over the parts in turn, the head over the lanes.
+// Joins the parts of tiles that were cut, rows shared evenly by the workgroups.
+// A group of D / 4 lanes holds four columns each of a row. Few parts: every
+// group has a row of its own. Many: the groups share one row, each takes its
+// share of the parts, and the shares join through LDS. A part without a key
+// of the row has l = 0 (and NaN scores leave m at -infinity, but not l at 0).
+struct Joined {
+    float m = -INFINITY, l = 0.f;
+    f32x4 v = zero4();
+    __device__ void add(const Joined& x) {
+        const bool none = x.l == 0.f;
+        const float mn = none ? m : fmaxf(m, x.m);
+        const float c = m == -INFINITY ? 1.f : exp2_f(m - mn);
+        const float c1 = none ? 0.f : x.m == -INFINITY ? 1.f : exp2_f(x.m - mn);
+        l = l * c + x.l * c1;
+        for (int i = 0; i < 4; ++i) v[i] = v[i] * c + (none ? 0.f : x.v[i] * c1);
+        m = mn;
+    }
+};
+
 template <typename T, int D>
-__global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit s, int per) {
-    __shared__ AttnSchedLds sched;
-    __shared__ float part[4][D], part_l[4], red[4];
-    const unsigned per_tile = (unsigned)(s.R / per);
-    const AttnItem it = attn_item<true>(a, s, blockIdx.x / per_tile, sched);
-    if (!it.found) return;
-    const int G = a.Hq / a.Hkv, row0 = (int)(blockIdx.x % per_tile) * per;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const long step = (long)it.tiles * a.Hkv;
-    const long slot = it.slot + (long)it.tile * a.Hkv + it.h;
-    if (slot + step * (it.parts - 1) >= s.slots) return;
-    constexpr int PER = D < 64 ? 1 : D / 64;
-    for (int row = row0; row < row0 + per; ++row) {
-        const RowAt x = row_at(a, it, G, it.tile * s.R + row);
-        if (!x.in) return;
-        auto row_of = [&](int p) { return (slot + step * p) * s.R + row; };
-        float m = -INFINITY;
-        for (int p = tid; p < it.parts; p += kAttnThreads) m = fmaxf(m, s.ml[row_of(p) * 2]);
-        for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-        if (lane == 0) red[w] = m;
-        __syncthreads();
-        m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        float l = 0.f, v[PER] = {};
-        for (int p = w; p < it.parts; p += 4) {
-            const float mp = s.ml[row_of(p) * 2], lp = s.ml[row_of(p) * 2 + 1];
-            if (lp == 0.f) continue;                 // a part without a key of this row
-            const float c = mp == -INFINITY ? 1.f : exp2_f(mp - m);
-            l += c * lp;
-            if (lane * PER < D)
-                for (int i = 0; i < PER; ++i) v[i] += c * s.acc[row_of(p) * D + lane * PER + i];
+__global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit s) {
+    constexpr int kLanes = D / 4, kGroups = kAttnThreads / kLanes;
+    __shared__ __align__(16) float lds_v[kGroups][D];
+    __shared__ float lds_ml[kGroups][2];
+    const int G = a.Hq / a.Hkv;
+    const int group = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+    __shared__ AttnItem shared_item;
+    __shared__ int shared_units;
+    AttnSched<true> sched;
+    if (wave_id() == 0) {
+        sched.init(a, s);
+        if (threadIdx.x == 0) shared_units = sched.items;
+    }
+    __syncthreads();
+    // an even share of the rows of all cut tiles, at most 2^12 tiles * 2^8
+    const unsigned all = (unsigned)uniform(shared_units) << s.R_log2;
+    const unsigned share = (all + gridDim.x - 1) / gridDim.x;
+    const unsigned row_end = min(all, share * (blockIdx.x + 1));
+    for (unsigned r = share * blockIdx.x; r < row_end;) {
+        const int x = (int)(r >> s.R_log2), row0 = (int)(r & (s.R - 1));
+        __syncthreads();                             // the last item is read
+        if (wave_id() == 0) sched.find(a, s, x, &shared_item);
+        const AttnItem it = attn_shared(shared_item);
+        const int rows = (int)min((unsigned)(s.R - row0), row_end - r);
+        r += rows;
+        const int step = it.tiles * a.Hkv, slot = it.slot + it.tile * a.Hkv + it.h;
+        // (only where offsets decrease)
+        if (!it.found || slot < 0 || slot + (long)step * (it.parts - 1) >= s.slots) continue;
+        const int have = min(rows, it.n * G - (it.tile * s.R + row0));   // rows that exist
+        // parts p, p + by, ... of a row; eight at a time in flight
+        auto gather = [&](int row, int p, int by) {
+            Joined y;
+            for (; p < it.parts; p += 8 * by) {
+                Joined z[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const bool in = p + i * by < it.parts;
+                    const long at = (long)(slot + step * (in ? p + i * by : p)) * s.R + row;
+                    z[i].m = s.ml[at * 2];
+                    z[i].l = s.ml[at * 2 + 1];
+                    z[i].v = *(const f32x4*)(s.acc + at * D + d);
+                    if (!in) z[i].l = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y.add(z[i]);
+            }
+            return y;
+        };
+        auto write = [&](const Joined& y, int row) {
+            const RowAt to = row_at(a, it, G, it.tile * s.R + row);
+            const float inv = y.l == 0.f ? 0.f : 1.f / y.l;
+            T* o = (T*)a.o + to.q * D + d;
+            for (int i = 0; i < 4; ++i) o[i] = from_f32<T>(y.v[i] * inv);
+            if (a.lse && d == 0) a.lse[to.q] = y.l == 0.f ? -INFINITY : (y.m + __log2f(y.l)) * kLn2;
+        };
+        if (it.parts <= 8) {
+            for (int row = group; row < have; row += kGroups) write(gather(row0 + row, 0, 1), row0 + row);
+            continue;
         }
-        if (lane * PER < D)
-            for (int i = 0; i < PER; ++i) part[w][lane * PER + i] = v[i];
-        if (lane == 0) part_l[w] = l;
-        __syncthreads();
-        l = part_l[0] + part_l[1] + part_l[2] + part_l[3];
-        if (tid < D) {
-            const float o = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
-            ((T*)a.o)[x.q * D + tid] = from_f32<T>(l == 0.f ? 0.f : o / l);
+        for (int row = 0; row < have; ++row) {
+            const Joined y = gather(row0 + row, group, kGroups);
+            __syncthreads();                         // the last row's shares are read
+            *(f32x4*)&lds_v[group][d] = y.v;
+            if (d == 0) { lds_ml[group][0] = y.m; lds_ml[group][1] = y.l; }
+            __syncthreads();
+            if (group == 0) {
+                Joined z;
+                for (int g = 0; g < kGroups; ++g) {
+                    Joined x1;
+                    x1.m = lds_ml[g][0];
+                    x1.l = lds_ml[g][1];
+                    x1.v = *(const f32x4*)&lds_v[g][d];
+                    z.add(x1);
+                }
+                write(z, row0 + row);
+            }
         }
-        if (a.lse && tid == 0) a.lse[x.q] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
-        __syncthreads();                             // part, part_l and red are free again
     }
 }
 
@@ -832,7 +867,6 @@ constexpr int kStreamRows = 32;
 struct Launch {
     AttnSplit split;
     long items, joins;     // workgroups
-    int per;               // rows a joining workgroup takes
 };
 struct Plan {
     int n;                 // launches
@@ -844,6 +878,7 @@ struct Plan {
 Launch launch_of(long T, long B, long G, long Hkv, int R, int unit, int target_log2) {
     Launch l{};
     l.split.R = R;
+    l.split.R_log2 = __builtin_ctz((unsigned)R);
     l.split.min_rows = 1;
     l.split.max_rows = INT32_MAX;
     l.split.unit = unit;
@@ -851,11 +886,9 @@ Launch launch_of(long T, long B, long G, long Hkv, int R, int unit, int target_l
     const long target = 1l << target_log2, tiles = attn_max_tiles(T, B, G, Hkv, R);
     l.items = attn_max_items(tiles, target);
     l.split.slots = (int)attn_max_slots(target);
-    // about 1024 workgroups for the joining: with fewer rows they take one each
+    // the joining's share of a row or more each
     const long rows = (tiles < target ? tiles : target) * R;
-    l.per = 1;
-    while (l.per < R && rows / l.per > 1024) l.per *= 2;
-    l.joins = rows / l.per;
+    l.joins = rows < 2048 ? rows : 2048;
     return l;
 }
 Plan plan_of(int T, int B, int Hq, int Hkv, int d, int max_new, bool bf16_io) {
@@ -908,8 +941,8 @@ hipError_t launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
             launch_stream<D>(a, p, l, st);
         }
         const unsigned n = (unsigned)l.joins;
-        if (a.bf16_io) attn_join<bf16, D><<<n, kAttnThreads, 0, st>>>(a, l.split, l.per);
-        else attn_join<float, D><<<n, kAttnThreads, 0, st>>>(a, l.split, l.per);
+        if (a.bf16_io) attn_join<bf16, D><<<n, kAttnThreads, 0, st>>>(a, l.split);
+        else attn_join<float, D><<<n, kAttnThreads, 0, st>>>(a, l.split);
     }
     return hipGetLastError();
 }

@@ -3,12 +3,14 @@
 // The n new tokens of a request and the G query heads of a KV head form n * G
 // rows (row r: token r / G, head r % G), cut into tiles of R rows. A tile's
 // keys are cut into parts of C keys, C such that all tiles of the call make
-// about `target` parts: one part per tile when there are tiles enough,
+// about 2^target_log2 parts: one part per tile when there are tiles enough,
 // many when few long requests have to fill the card. Lengths are on the
-// device, so each workgroup reads them (B of each, coalesced), sums the work
-// and finds its part in the prefix sums: about 2 us, most of it hidden by the
-// other workgroups of its compute unit, against about 5 us for a kernel of
-// its own that writes the list. The grid is what the host can bound.
+// device, so the first wave of each workgroup reads them, four requests a
+// lane, sums the work and finds its part in the prefix sums, in registers:
+// about 300 instructions up to 256 requests, where a kernel that writes the
+// list first would cost every call a launch. (All four waves doing it spent
+// more time on it than on small calls' keys.) The grid is what the host can
+// bound.
 #pragma once
 
 #include "kda_serve_launch.h"
@@ -20,7 +22,7 @@ constexpr int kAttnThreads = 256;
 
 // What a launch works on, besides AttnArgs.
 struct AttnSplit {
-    int R;              // rows of a tile
+    int R, R_log2;      // rows of a tile, a power of two
     int min_rows;       // only requests of at least min_rows rows ...
     int max_rows;       // ... and at most max_rows of them
     int unit;           // granularity and least length of a part, a power of two
@@ -36,108 +38,210 @@ struct AttnItem {
     int n;              // its new tokens
     int kept;           // its tokens before them
     int C;              // keys of a part
-    long slot;          // partial result of part 0, tile 0, head 0
+    int slot;           // partial result of part 0, tile 0, head 0
     bool found;
 };
 
 struct AttnReq { int n, kv, tiles, row0, kept; };
 
-__device__ __forceinline__ AttnReq attn_req(const AttnArgs& a, const AttnSplit& s, int i) {
-    AttnReq r{0, 0, 0, 0, 0};
-    if (i >= a.B) return r;
-    int lo = a.cu[i], hi = a.cu[i + 1];
+// A request from its offsets and length as they are stored; in = false: none.
+__device__ __forceinline__ AttnReq attn_req(const AttnArgs& a, const AttnSplit& s, bool in, int lo,
+                                            int hi, int kept) {
+    AttnReq r;
     lo = min(max(lo, 0), a.T);
     hi = min(max(hi, 0), a.T);
-    const int cap = a.width << a.page_shift;
+    const int cap = a.width << a.page_shift;         // at most 2^30, as T is
     r.row0 = lo;
-    r.n = max(hi - lo, 0);
-    r.kept = min(max(a.kept[i], 0), cap);
-    r.kv = min(r.kept + (long)r.n, (long)cap);
-    const long rows = (long)r.n * (a.Hq / a.Hkv);
-    r.tiles = rows >= s.min_rows && rows <= s.max_rows ? (int)((rows + s.R - 1) / s.R) : 0;
+    r.n = in ? max(hi - lo, 0) : 0;
+    r.kept = min(max(kept, 0), cap);
+    r.kv = min(r.kept + r.n, cap);
+    const int rows = r.n * (a.Hq / a.Hkv);           // at most T Hq
+    r.tiles = rows >= s.min_rows && rows <= s.max_rows ? (rows + s.R - 1) >> s.R_log2 : 0;
     return r;
 }
 
-struct AttnSchedLds { long wave[2][kAttnThreads / 64]; AttnItem item; long cost; };
-
-// Exclusive prefix and total of two counters over the workgroup.
-__device__ __forceinline__ void attn_scan(long& x, long& y, long& tx, long& ty, AttnSchedLds& lds) {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    long ix = x, iy = y;
-    for (int o = 1; o < 64; o <<= 1) {
-        const long px = __shfl_up(ix, o), py = __shfl_up(iy, o);
-        if (lane >= o) { ix += px; iy += py; }
-    }
-    __syncthreads();
-    if (lane == 63) { lds.wave[0][w] = ix; lds.wave[1][w] = iy; }
-    __syncthreads();
-    tx = ty = 0;
-    x = ix - x;
-    y = iy - y;
-    for (int i = 0; i < kAttnThreads / 64; ++i) {
-        if (i < w) { x += lds.wave[0][i]; y += lds.wave[1][i]; }
-        tx += lds.wave[0][i];
-        ty += lds.wave[1][i];
-    }
+// Inclusive prefix sum over the wave: shifts inside each 16-lane row, then
+// the last lane of row 0 (2) into row 1 (3) and of row 1 into rows 2 and 3.
+__device__ __forceinline__ int wave_prefix(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
+    return x;
 }
 
-// The x-th part of the call (UNITS = false), or the x-th tile of those that
-// were cut into several parts (UNITS = true: for joining them).
+// 256 requests of one wave, four a lane: what they were cut into. UNITS
+// counts the tiles that were cut (for joining them), otherwise the parts.
 template <bool UNITS>
-__device__ __forceinline__ AttnItem attn_item(const AttnArgs& a, const AttnSplit& s, long x,
-                                              AttnSchedLds& lds) {
-    const int tid = threadIdx.x;
-    AttnReq first = attn_req(a, s, tid);
-    long cost = (long)first.tiles * first.kv;
-    for (int i = tid + kAttnThreads; i < a.B; i += kAttnThreads) {
-        const AttnReq r = attn_req(a, s, i);
-        cost += (long)r.tiles * r.kv;
+struct AttnBlock {
+    AttnReq r0, r1, r2, r3;
+    int p0, p1, p2, p3;      // parts of a tile
+    int f1, f2, f3, mine, p; // items before the 2nd .. 4th request, in all, and the prefix
+    int c1, c2, c3, cut, q;  // the same for partial results
+
+    __device__ void load(const AttnArgs& a, const AttnSplit& s, int base) {
+        // no branch between the loads: one memory latency for all nine
+        const int i = base + 4 * (threadIdx.x & 63), last = a.B - 1;
+        const int u0 = a.cu[min(i, a.B)], u1 = a.cu[min(i + 1, a.B)], u2 = a.cu[min(i + 2, a.B)],
+                  u3 = a.cu[min(i + 3, a.B)], u4 = a.cu[min(i + 4, a.B)];
+        const int k0 = a.kept[min(i, last)], k1 = a.kept[min(i + 1, last)],
+                  k2 = a.kept[min(i + 2, last)], k3 = a.kept[min(i + 3, last)];
+        r0 = attn_req(a, s, i <= last, u0, u1, k0);
+        r1 = attn_req(a, s, i + 1 <= last, u1, u2, k1);
+        r2 = attn_req(a, s, i + 2 <= last, u2, u3, k2);
+        r3 = attn_req(a, s, i + 3 <= last, u3, u4, k3);
     }
-    long zero = 0, total, none;
-    attn_scan(cost, zero, total, none, lds);
-    // a part covers at most all positions, which fit 31 bits
-    const long want = (total * a.Hkv) >> s.target_log2;
-    const int C = (int)min((want & ~(long)(s.unit - 1)) + s.unit, (long)INT32_MAX);
-    if (tid == 0) lds.item.found = false;
-    long at = 0, slot0 = 0;
-    for (int base = 0; base < a.B; base += kAttnThreads) {
-        const AttnReq r = base == 0 ? first : attn_req(a, s, base + tid);
-        const unsigned parts = r.kv > C ? ((unsigned)r.kv + (unsigned)C - 1) / (unsigned)C : 1;
-        const long tiles = (long)r.tiles * a.Hkv;
-        const long here = parts * tiles;
-        const long mine = UNITS ? (parts > 1 ? tiles : 0) : here;
-        long p = mine, q = parts > 1 ? here : 0, tp, tq;
-        attn_scan(p, q, tp, tq, lds);
-        if (x >= at + p && x < at + p + mine) {
-            const unsigned local = (unsigned)(x - at - p), rest = local / (unsigned)a.Hkv;
-            AttnItem it;
-            it.req = base + tid;
-            it.h = (int)(local % (unsigned)a.Hkv);
-            // the last tile first: it sees the most keys
-            it.tile = r.tiles - 1 - (int)(rest % (unsigned)r.tiles);
-            it.part = (int)(rest / (unsigned)r.tiles);
-            it.parts = (int)parts;
-            it.tiles = r.tiles;
-            it.row0 = r.row0;
-            it.n = r.n;
-            it.kept = r.kept;
-            it.C = C;
-            it.slot = slot0 + q;
-            it.found = true;
-            lds.item = it;
+    __device__ float cost() const {
+        return (float)r0.tiles * (float)r0.kv + (float)r1.tiles * (float)r1.kv +
+               ((float)r2.tiles * (float)r2.kv + (float)r3.tiles * (float)r3.kv);
+    }
+    // ceil(kv / C) in fp32: C is a multiple of 64, so the quotient is off by
+    // less than 2^-24 * 2^24 / 64 and one comparison mends it
+    static __device__ int parts(int kv, int C, float rC) {
+        int n = (int)((float)kv * rC);
+        n = max(n, 1);
+        if ((long)n * C < kv) ++n;
+        if ((long)(n - 1) * C >= kv && n > 1) --n;
+        return n;
+    }
+    __device__ void split(const AttnArgs& a, int C) {
+        const float rC = 1.f / (float)C;
+        p0 = parts(r0.kv, C, rC);
+        p1 = parts(r1.kv, C, rC);
+        p2 = parts(r2.kv, C, rC);
+        p3 = parts(r3.kv, C, rC);
+        const int t0 = r0.tiles * a.Hkv, t1 = r1.tiles * a.Hkv, t2 = r2.tiles * a.Hkv,
+                  t3 = r3.tiles * a.Hkv;
+        const auto items = [](int t, int n) { return UNITS ? (n == 1 ? 0 : t) : t * n; };
+        const auto cuts = [](int t, int n) { return n == 1 ? 0 : t * n; };
+        f1 = items(t0, p0);
+        f2 = f1 + items(t1, p1);
+        f3 = f2 + items(t2, p2);
+        mine = f3 + items(t3, p3);
+        c1 = cuts(t0, p0);
+        c2 = c1 + cuts(t1, p1);
+        c3 = c2 + cuts(t2, p2);
+        cut = c3 + cuts(t3, p3);
+        p = wave_prefix(mine);
+        q = wave_prefix(cut);
+    }
+    __device__ int items() const { return __builtin_amdgcn_readlane(p, 63); }
+    __device__ int slots() const { return __builtin_amdgcn_readlane(q, 63); }
+    // Item y of these, 0 <= y < items(): the lane that has it writes it down.
+    __device__ void find(const AttnArgs& a, int base, int y, int slot0, int C, AttnItem* to) const {
+        const int local = y - (p - mine);
+        if (local < 0 || local >= mine) return;
+        // (a request without items begins where the next one does)
+        const bool b1 = local >= f1, b2 = local >= f2, b3 = local >= f3;
+        const auto of = [&](int x0, int x1, int x2, int x3) { return b3 ? x3 : b2 ? x2 : b1 ? x1 : x0; };
+        const int tiles = of(r0.tiles, r1.tiles, r2.tiles, r3.tiles), n = of(p0, p1, p2, p3);
+        const unsigned k = (unsigned)(local - of(0, f1, f2, f3)), rest = k / (unsigned)a.Hkv;
+        const unsigned part = rest / (unsigned)max(tiles, 1);
+        to->req = base + 4 * (int)(threadIdx.x & 63) + of(0, 1, 2, 3);
+        to->h = (int)(k - rest * (unsigned)a.Hkv);
+        // the last tile first: it sees the most keys
+        to->tile = tiles - 1 - (int)(rest - part * (unsigned)tiles);
+        to->part = (int)part;
+        to->parts = n;
+        to->tiles = tiles;
+        to->row0 = of(r0.row0, r1.row0, r2.row0, r3.row0);
+        to->n = of(r0.n, r1.n, r2.n, r3.n);
+        to->kept = of(r0.kept, r1.kept, r2.kept, r3.kept);
+        to->C = C;
+        to->slot = slot0 + q - cut + of(0, c1, c2, c3);
+        to->found = tiles > 0 && (int)part < n;
+    }
+};
+
+// The first wave's view of the call. Every workgroup of every kernel of a call
+// computes the same C: the sum of the work runs in fp32 in a fixed order, and
+// the bounds below leave room for its rounding.
+template <bool UNITS>
+struct AttnSched {
+    AttnBlock<UNITS> first;
+    int C, items;
+
+    __device__ void init(const AttnArgs& a, const AttnSplit& s) {
+        first.load(a, s, 0);
+        float cost = first.cost();
+        for (int base = 256; base < a.B; base += 256) {
+            AttnBlock<UNITS> b;
+            b.load(a, s, base);
+            cost += b.cost();
         }
-        at += tp;
-        slot0 += tq;
-        if (x < at) break;                 // the same for every thread
+        const float want = wave_sum_uniform(cost) * (float)a.Hkv *
+                           __builtin_bit_cast(float, (127 - s.target_log2) << 23);
+        // a part covers at most all positions
+        C = __builtin_amdgcn_readfirstlane(((int)fminf(want, 1073741824.f) & ~(s.unit - 1)) + s.unit);
+        first.split(a, C);
+        items = first.items();
+        if (UNITS)
+            for (int base = 256; base < a.B; base += 256) {
+                AttnBlock<UNITS> b;
+                b.load(a, s, base);
+                b.split(a, C);
+                items += b.items();
+            }
     }
+    // The y-th item of the call into LDS; found = false behind the last.
+    __device__ void find(const AttnArgs& a, const AttnSplit& s, int y, AttnItem* to) const {
+        if (threadIdx.x == 0) to->found = false;
+        int at = first.items(), slot0 = first.slots();
+        if (y < at) {
+            first.find(a, 0, y, 0, C, to);
+            return;
+        }
+        for (int base = 256; base < a.B; base += 256) {
+            AttnBlock<UNITS> b;
+            b.load(a, s, base);
+            b.split(a, C);
+            const int n = b.items();
+            if (y < at + n) {
+                b.find(a, base, y - at, slot0, C, to);
+                return;
+            }
+            at += n;
+            slot0 += b.slots();
+        }
+    }
+};
+
+// The item that the first wave wrote down, for the whole workgroup.
+__device__ __forceinline__ AttnItem attn_shared(const AttnItem& lds) {
     __syncthreads();
-    return lds.item;
+    AttnItem it = lds;
+    it.req = __builtin_amdgcn_readfirstlane(it.req);
+    it.h = __builtin_amdgcn_readfirstlane(it.h);
+    it.tile = __builtin_amdgcn_readfirstlane(it.tile);
+    it.part = __builtin_amdgcn_readfirstlane(it.part);
+    it.parts = __builtin_amdgcn_readfirstlane(it.parts);
+    it.tiles = __builtin_amdgcn_readfirstlane(it.tiles);
+    it.row0 = __builtin_amdgcn_readfirstlane(it.row0);
+    it.n = __builtin_amdgcn_readfirstlane(it.n);
+    it.kept = __builtin_amdgcn_readfirstlane(it.kept);
+    it.C = __builtin_amdgcn_readfirstlane(it.C);
+    it.slot = __builtin_amdgcn_readfirstlane(it.slot);
+    it.found = __builtin_amdgcn_readfirstlane((int)it.found) != 0;
+    return it;
+}
+
+// The x-th part of the call.
+__device__ __forceinline__ AttnItem attn_item(const AttnArgs& a, const AttnSplit& s, int x,
+                                              AttnItem& lds) {
+    if (wave_id() == 0) {
+        AttnSched<false> sched;
+        sched.init(a, s);
+        sched.find(a, s, x, &lds);
+    }
+    return attn_shared(lds);
 }
 
 // Bounds of the host: parts of a call whose tiles number at most `tiles`
 // (KV heads included), and partial results.
-inline long attn_max_items(long tiles, long target) { return tiles + target; }
-inline long attn_max_slots(long target) { return 2 * target; }
+inline long attn_max_items(long tiles, long target) { return tiles + target + 16; }
+inline long attn_max_slots(long target) { return 2 * target + 16; }
 inline long attn_max_tiles(long T, long B, long G, long Hkv, long R) {
     return (T * G / R + (B < T ? B : T)) * Hkv;
 }

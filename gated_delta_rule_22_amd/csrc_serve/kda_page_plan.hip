@@ -25,24 +25,71 @@ struct PlanWs {
         : have((int*)ws), taken(have + B), given(taken + B + 1), ring(given + B + 1) {}
 };
 
-// Inclusive prefix sums of v over the workgroup, and the total.
-template <typename T>
-__device__ T block_scan(T v, T* lds, T& total) {
+// Inclusive prefix sum over the wave: shifts inside each 16-lane row, then
+// the last lane of row 0 (2) into row 1 (3) and of row 1 into rows 2 and 3.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ long dpp_add(long x) {
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(x >> 32), CTRL, ROWS, 0xF, false);
+    return x + (long)((unsigned long)(unsigned)lo | (unsigned long)(unsigned)hi << 32);
+}
+__device__ __forceinline__ long wave_prefix(long x) {
+    x = dpp_add<0x111, 0xF>(x);
+    x = dpp_add<0x112, 0xF>(x);
+    x = dpp_add<0x114, 0xF>(x);
+    x = dpp_add<0x118, 0xF>(x);
+    x = dpp_add<0x142, 0xA>(x);
+    return dpp_add<0x143, 0xC>(x);
+}
+
+// Tokens, pages taken and pages given back of some requests; bad: one of
+// them has a value outside its range.
+struct Counts {
+    long tokens, taken, given;
+    int bad;
+};
+// Inclusive prefix sums over the workgroup, and the totals. 64 bits: the
+// inputs are anything.
+__device__ __forceinline__ Counts block_prefix(Counts c, Counts* lds, Counts& total) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    for (int o = 1; o < 64; o <<= 1) {
-        const T x = __shfl_up(v, o);
-        if (lane >= o) v += x;
-    }
+    c.tokens = wave_prefix(c.tokens);
+    c.taken = wave_prefix(c.taken);
+    c.given = wave_prefix(c.given);
+    c.bad = __any(c.bad);
     __syncthreads();                     // lds free of an earlier call's reads
-    if (lane == 63) lds[w] = v;
+    if (lane == 63) lds[w] = c;
     __syncthreads();
-    T before = 0, all = 0;
-    for (int i = 0; i < (int)(blockDim.x >> 6); ++i) {
-        if (i < w) before += lds[i];
-        all += lds[i];
-    }
-    total = all;
-    return v + before;
+    // the waves' sums, one a lane, and their prefix
+    Counts t = lds[lane < kThreads / 64 ? lane : 0];
+    if (lane >= kThreads / 64) t = Counts{0, 0, 0, 0};
+    const Counts own = t;
+    t.tokens = wave_prefix(t.tokens);
+    t.taken = wave_prefix(t.taken);
+    t.given = wave_prefix(t.given);
+    total.tokens = __shfl(t.tokens, 63);
+    total.taken = __shfl(t.taken, 63);
+    total.given = __shfl(t.given, 63);
+    total.bad = __any(t.bad);
+    c.tokens += __shfl(t.tokens - own.tokens, w);
+    c.taken += __shfl(t.taken - own.taken, w);
+    c.given += __shfl(t.given - own.given, w);
+    return c;
+}
+
+// A request: what it holds and needs.
+struct Request { int have, need; Counts c; };
+__device__ __forceinline__ Request request(const PlanArgs& a, int i) {
+    Request r{0, 0, {0, 0, 0, 0}};
+    if (i >= a.B) return r;
+    const long kept = a.kept[i], fresh = a.fresh[i], have = a.pages_in[i];
+    const long need = (kept + fresh + (1l << a.page_shift) - 1) >> a.page_shift;
+    r.c.bad = kept < 0 || fresh < 0 || have < 0 || have > a.width || need > a.width;
+    r.have = (int)have;
+    r.need = (int)need;
+    r.c.tokens = fresh;
+    r.c.taken = need > have ? need - have : 0;
+    r.c.given = have > need ? have - need : 0;
+    return r;
 }
 
 // Largest i with off[i] <= x, for off[0] = 0 <= x < off[n].
@@ -86,75 +133,60 @@ __device__ void fill(const PlanArgs& a, const PlanWs& w, long first, long step) 
 }
 
 __global__ __launch_bounds__(kThreads) void page_plan_scan(PlanArgs a, void* ws, bool fill_too) {
-    __shared__ long lds_l[kThreads / 64];
-    __shared__ int lds_i[kThreads / 64];
+    __shared__ Counts lds[kThreads / 64];
     const PlanWs w(ws, a.B);
     const int head = a.ring_in[0], count = a.ring_in[1];
-    const long page = 1l << a.page_shift;
-    long tokens = 0, taken = 0, given = 0;
-    int bad = 0;
-    for (int i = threadIdx.x; i < a.B; i += kThreads) {
-        const long kept = a.kept[i], fresh = a.fresh[i], have = a.pages_in[i];
-        const long need = (kept + fresh + page - 1) >> a.page_shift;
-        bad |= kept < 0 || fresh < 0 || have < 0 || have > a.width || need > a.width;
-        tokens += fresh;
-        taken += need > have ? need - have : 0;
-        given += have > need ? have - need : 0;
+    // up to kThreads requests are read and summed once; more are summed first
+    Request r = request(a, threadIdx.x);
+    Counts all, p = block_prefix(r.c, lds, all);
+    for (int base = kThreads; base < a.B; base += kThreads) {
+        Counts t;
+        block_prefix(request(a, base + (int)threadIdx.x).c, lds, t);
+        all.tokens += t.tokens;
+        all.taken += t.taken;
+        all.given += t.given;
+        all.bad |= t.bad;
     }
-    long n_tokens, n_taken, n_given, n_bad;
-    block_scan<long>(tokens, lds_l, n_tokens);
-    block_scan<long>(taken, lds_l, n_taken);
-    block_scan<long>(given, lds_l, n_given);
-    block_scan<long>((long)bad, lds_l, n_bad);
     // Given-back entries land behind the free ones and never on an entry that
     // is taken in this call, because free and given-back pages together fit
     // the ring; more of them means that a page is held twice.
     int status = KDA_PLAN_OK;
-    if (n_bad || head < 0 || count < 0 || count > a.pool || head >= (a.pool > 0 ? a.pool : 1) ||
-        count + n_given > a.pool)
+    if (all.bad || head < 0 || count < 0 || count > a.pool || head >= (a.pool > 0 ? a.pool : 1) ||
+        count + all.given > a.pool)
         status = KDA_PLAN_INVALID;
-    else if (n_tokens > a.n_slots)
+    else if (all.tokens > a.n_slots)
         status = KDA_PLAN_NO_SLOTS;
-    else if (n_taken > count)
-        status = n_taken - count > INT32_MAX ? INT32_MAX : (int)(n_taken - count);
+    else if (all.taken > count)
+        status = all.taken - count > INT32_MAX ? INT32_MAX : (int)(all.taken - count);
     const bool ok = status == KDA_PLAN_OK;
-    int cu0 = 0, taken0 = 0, given0 = 0;
+    int tokens0 = 0, taken0 = 0, given0 = 0;
     for (int base = 0; base < a.B; base += kThreads) {
         const int i = base + (int)threadIdx.x;
-        int fresh = 0, plus = 0, minus = 0, have = 0, need = 0;
-        if (i < a.B) {
-            have = a.pages_in[i];
-            need = have;
-            if (ok) {
-                fresh = a.fresh[i];
-                need = (int)(((long)a.kept[i] + fresh + page - 1) >> a.page_shift);
-                plus = need > have ? need - have : 0;
-                minus = have > need ? have - need : 0;
-            }
+        Counts t = all;
+        if (a.B > kThreads) {
+            r = request(a, i);
+            p = block_prefix(r.c, lds, t);
         }
-        int t_fresh, t_plus, t_minus;
-        const int s_fresh = block_scan<int>(fresh, lds_i, t_fresh);
-        const int s_plus = block_scan<int>(plus, lds_i, t_plus);
-        const int s_minus = block_scan<int>(minus, lds_i, t_minus);
         if (i < a.B) {
-            w.have[i] = have;
-            w.taken[i] = taken0 + s_plus - plus;
-            w.given[i] = given0 + s_minus - minus;
-            a.cu[i] = cu0 + s_fresh - fresh;
-            a.pages_out[i] = need;
+            w.have[i] = r.have;
+            w.taken[i] = ok ? taken0 + (int)(p.taken - r.c.taken) : 0;
+            w.given[i] = ok ? given0 + (int)(p.given - r.c.given) : 0;
+            a.cu[i] = ok ? tokens0 + (int)(p.tokens - r.c.tokens) : 0;
+            a.pages_out[i] = ok ? r.need : r.have;
         }
-        cu0 += t_fresh;
-        taken0 += t_plus;
-        given0 += t_minus;
+        tokens0 += (int)t.tokens;
+        taken0 += (int)t.taken;
+        given0 += (int)t.given;
     }
     if (threadIdx.x == 0) {
-        w.taken[a.B] = taken0;
-        w.given[a.B] = given0;
+        const int taken = ok ? (int)all.taken : 0, given = ok ? (int)all.given : 0;
+        w.taken[a.B] = taken;
+        w.given[a.B] = given;
         w.ring[0] = head;
         w.ring[1] = count;
-        a.cu[a.B] = cu0;
-        a.ring_out[0] = taken0 ? (int)(((long)head + taken0) % a.pool) : head;
-        a.ring_out[1] = count - taken0 + given0;
+        a.cu[a.B] = ok ? (int)all.tokens : 0;
+        a.ring_out[0] = taken ? (int)(((long)head + taken) % a.pool) : head;
+        a.ring_out[1] = count - taken + given;
         a.status[0] = status;
     }
     if (fill_too) {

@@ -10,6 +10,7 @@ this order in a step; the verification's ``n_commit`` is the one that
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -37,10 +38,15 @@ def declare(lib) -> None:
     lib.kda_draft_verify.restype = i
 
 
+# A serving step makes these calls once per layer: the checks below cost about
+# 0.3 us a tensor where the package's general one (which words the refusal)
+# takes 1 us, and a call on the current device needs no device switch.
+
 def _device(t: torch.Tensor, what: str) -> torch.device:
-    if t.device.type != "cuda":
+    dev = t.device
+    if dev.type != "cuda":
         raise ValueError(f"{what} needs GPU tensors")
-    return t.device
+    return dev
 
 
 def _dtype(t: torch.Tensor) -> torch.dtype:
@@ -55,33 +61,43 @@ def _dims(t: torch.Tensor, name: str, n: int):
     return t.shape
 
 
-def _out(t: Optional[torch.Tensor], name: str, shape, dtype, dev, stream) -> torch.Tensor:
-    """The caller's output, checked, or a new one."""
-    if t is None:
-        return _kda._empty(shape, dtype, dev, stream)
-    _kda._check(t, name, shape, dtype, dev)
-    return t
+def _ptr(t: torch.Tensor, name: str, shape, dtype, dev) -> int:
+    """The address of a tensor that is as it has to be."""
+    if t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        _kda._check(t, name, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _out(t: Optional[torch.Tensor], shape, dtype, dev, stream) -> torch.Tensor:
+    """The caller's output, or a new one."""
+    return _kda._empty(shape, dtype, dev, stream) if t is None else t
 
 
 def _workspace(ws: Optional[torch.Tensor], need: int, dev, stream):
-    """(workspace or None, its bytes): the caller's if it is large enough."""
+    """(workspace or None, its address, its bytes): the caller's if it is large enough."""
     if ws is not None:
         if ws.device != dev:
             raise ValueError(f"workspace is on {ws.device}, expected {dev}")
         if not ws.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    if need and (ws is None or ws.numel() * ws.element_size() < need):
-        ws = _kda._empty(need, torch.uint8, dev, stream)
-    return ws, 0 if ws is None else ws.numel() * ws.element_size()
+    if need and (ws is None or ws.nbytes < need):
+        ws = _kda._empty((need,), torch.uint8, dev, stream)
+    return (None, None, 0) if ws is None else (ws, ws.data_ptr(), ws.nbytes)
 
 
-def _call(name: str, dev, *args) -> None:
-    with torch.cuda.device(dev):
-        st = getattr(_kda.load_library(), name)(*args)
+def _call(name: str, dev, stream, *args) -> None:
+    fn = getattr(_kda.load_library(), name)
+    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
     if st != 0:
         raise _kda.KDAError(st, name)
 
 
+@functools.lru_cache(maxsize=256)
 def kda_page_plan_workspace_size(B: int) -> int:
     return int(_kda.load_library().kda_page_plan_workspace_size(B))
 
@@ -108,25 +124,25 @@ def kda_page_plan(kept_len: torch.Tensor, n_new: torch.Tensor, n_pages: torch.Te
     B, = _dims(kept_len, "kept_len", 1)
     _, width = _dims(block_table, "block_table", 2)
     pool, = _dims(free_ring, "free_ring", 1)
-    for t, name, shape in ((kept_len, "kept_len", (B,)), (n_new, "n_new", (B,)),
-                           (n_pages, "n_pages", (B,)),
-                           (block_table, "block_table", (B, width)),
-                           (free_ring, "free_ring", (pool,)), (ring, "ring", (2,))):
-        _kda._check(t, name, shape, i32, dev)
     if slot_map is None and n_slots is None:
         raise ValueError("kda_page_plan needs n_slots or slot_map")
     if n_slots is None:
         n_slots, = _dims(slot_map, "slot_map", 1)
-    n_pages_out = _out(n_pages_out, "n_pages_out", (B,), i32, dev, stream)
-    ring_out = _out(ring_out, "ring_out", (2,), i32, dev, stream)
-    cu_new = _out(cu_new, "cu_new", (B + 1,), i32, dev, stream)
-    slot_map = _out(slot_map, "slot_map", (n_slots,), i32, dev, stream)
-    status = _out(status, "status", (1,), i32, dev, stream)
-    ws, wsz = _workspace(workspace, kda_page_plan_workspace_size(B), dev, stream)
-    p = _kda._ptr
-    _call("kda_page_plan", dev, p(kept_len), p(n_new), p(n_pages), p(n_pages_out),
-          p(block_table), p(free_ring), p(ring), p(ring_out), p(cu_new), p(slot_map), p(status),
-          B, width, int(page_size), pool, int(n_slots), p(ws), wsz, _kda._stream(stream, dev))
+    n_pages_out = _out(n_pages_out, (B,), i32, dev, stream)
+    ring_out = _out(ring_out, (2,), i32, dev, stream)
+    cu_new = _out(cu_new, (B + 1,), i32, dev, stream)
+    slot_map = _out(slot_map, (n_slots,), i32, dev, stream)
+    status = _out(status, (1,), i32, dev, stream)
+    ws, wsp, wsz = _workspace(workspace, kda_page_plan_workspace_size(B), dev, stream)
+    _call("kda_page_plan", dev, stream, _ptr(kept_len, "kept_len", (B,), i32, dev),
+          _ptr(n_new, "n_new", (B,), i32, dev), _ptr(n_pages, "n_pages", (B,), i32, dev),
+          _ptr(n_pages_out, "n_pages_out", (B,), i32, dev),
+          _ptr(block_table, "block_table", (B, width), i32, dev),
+          _ptr(free_ring, "free_ring", (pool,), i32, dev), _ptr(ring, "ring", (2,), i32, dev),
+          _ptr(ring_out, "ring_out", (2,), i32, dev), _ptr(cu_new, "cu_new", (B + 1,), i32, dev),
+          _ptr(slot_map, "slot_map", (n_slots,), i32, dev),
+          _ptr(status, "status", (1,), i32, dev),
+          B, width, int(page_size), pool, int(n_slots), wsp, wsz)
     return cu_new, slot_map, n_pages_out, ring_out, status
 
 
@@ -137,16 +153,14 @@ def kda_cache_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
     dev, dt = _device(k, "kda_cache_append"), _dtype(k)
     T, H, d = _dims(k, "k", 3)
     pool, _, page, _ = _dims(k_cache, "k_cache", 4)
-    _kda._check(k, "k", (T, H, d), dt, dev)
-    _kda._check(v, "v", (T, H, d), dt, dev)
-    _kda._check(slot_map, "slot_map", (T,), torch.int32, dev)
-    _kda._check(k_cache, "k_cache", (pool, H, page, d), dt, dev)
-    _kda._check(v_cache, "v_cache", (pool, H, page, d), dt, dev)
-    p = _kda._ptr
-    _call("kda_cache_append", dev, p(k), p(v), p(slot_map), p(k_cache), p(v_cache), T, H, d, page,
-          pool, _kda._DTYPES[dt], _kda._stream(stream, dev))
+    rows, cache = (T, H, d), (pool, H, page, d)
+    _call("kda_cache_append", dev, stream, _ptr(k, "k", rows, dt, dev), _ptr(v, "v", rows, dt, dev),
+          _ptr(slot_map, "slot_map", (T,), torch.int32, dev),
+          _ptr(k_cache, "k_cache", cache, dt, dev), _ptr(v_cache, "v_cache", cache, dt, dev),
+          T, H, d, page, pool, _kda._DTYPES[dt])
 
 
+@functools.lru_cache(maxsize=256)
 def kda_attn_paged_workspace_size(T: int, B: int, Hq: int, Hkv: int, d: int, max_new: int,
                                   dtype: torch.dtype) -> int:
     return int(_kda.load_library().kda_attn_paged_workspace_size(T, B, Hq, Hkv, d, max_new,
@@ -169,24 +183,24 @@ def kda_attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     T, Hq, d = _dims(q, "q", 3)
     pool, Hkv, page, _ = _dims(k_cache, "k_cache", 4)
     B, width = _dims(block_table, "block_table", 2)
-    _kda._check(q, "q", (T, Hq, d), dt, dev)
-    _kda._check(k_cache, "k_cache", (pool, Hkv, page, d), dt, dev)
-    _kda._check(v_cache, "v_cache", (pool, Hkv, page, d), dt, dev)
-    _kda._check(block_table, "block_table", (B, width), torch.int32, dev)
-    _kda._check(kept_len, "kept_len", (B,), torch.int32, dev)
-    _kda._check(cu_new, "cu_new", (B + 1,), torch.int32, dev)
-    o = _out(o, "o", (T, Hq, d), dt, dev, stream)
-    if lse is not None or want_lse:
-        lse = _out(lse, "lse", (T, Hq), torch.float32, dev, stream)
+    i32, cache = torch.int32, (pool, Hkv, page, d)
+    o = _out(o, (T, Hq, d), dt, dev, stream)
+    if lse is None and want_lse:
+        lse = _kda._empty((T, Hq), torch.float32, dev, stream)
     need = kda_attn_paged_workspace_size(T, B, Hq, Hkv, d, max_new, dt)
-    ws, wsz = _workspace(workspace, need, dev, stream)
-    p = _kda._ptr
-    _call("kda_attn_paged", dev, p(q), p(k_cache), p(v_cache), p(block_table), p(kept_len),
-          p(cu_new), p(o), p(lse), T, B, Hq, Hkv, d, page, pool, width, int(max_new),
-          float(scale), _kda._DTYPES[dt], p(ws), wsz, _kda._stream(stream, dev))
+    ws, wsp, wsz = _workspace(workspace, need, dev, stream)
+    _call("kda_attn_paged", dev, stream, _ptr(q, "q", (T, Hq, d), dt, dev),
+          _ptr(k_cache, "k_cache", cache, dt, dev), _ptr(v_cache, "v_cache", cache, dt, dev),
+          _ptr(block_table, "block_table", (B, width), i32, dev),
+          _ptr(kept_len, "kept_len", (B,), i32, dev), _ptr(cu_new, "cu_new", (B + 1,), i32, dev),
+          _ptr(o, "o", (T, Hq, d), dt, dev),
+          None if lse is None else _ptr(lse, "lse", (T, Hq), torch.float32, dev),
+          T, B, Hq, Hkv, d, page, pool, width, int(max_new), float(scale), _kda._DTYPES[dt],
+          wsp, wsz)
     return o, lse
 
 
+@functools.lru_cache(maxsize=256)
 def kda_draft_verify_workspace_size(B: int, T: int, V: int) -> int:
     return int(_kda.load_library().kda_draft_verify_workspace_size(B, T, V))
 
@@ -209,18 +223,16 @@ def kda_draft_verify(target_probs: torch.Tensor, draft_probs: Optional[torch.Ten
     T = T1 - 1
     if T < 0:
         raise ValueError("target_probs needs T + 1 >= 1 rows per request")
-    _kda._check(target_probs, "target_probs", (B, T + 1, V), dt, dev)
-    if draft_probs is not None:
-        _kda._check(draft_probs, "draft_probs", (B, T, V), dt, dev)
-    _kda._check(draft_tokens, "draft_tokens", (B, T), torch.int32, dev)
-    _kda._check(u, "u", (B, T + 1), torch.float32, dev)
-    if n_draft is not None:
-        _kda._check(n_draft, "n_draft", (B,), torch.int32, dev)
-    n_commit = _out(n_commit, "n_commit", (B,), torch.int32, dev, stream)
-    tokens = _out(tokens, "tokens", (B, T + 1), torch.int32, dev, stream)
-    ws, wsz = _workspace(workspace, kda_draft_verify_workspace_size(B, T, V), dev, stream)
-    p = _kda._ptr
-    _call("kda_draft_verify", dev, p(target_probs), p(draft_probs), p(draft_tokens), p(u),
-          p(n_draft), p(n_commit), p(tokens), B, T, V, _kda._DTYPES[dt], p(ws), wsz,
-          _kda._stream(stream, dev))
+    i32 = torch.int32
+    n_commit = _out(n_commit, (B,), i32, dev, stream)
+    tokens = _out(tokens, (B, T1), i32, dev, stream)
+    ws, wsp, wsz = _workspace(workspace, kda_draft_verify_workspace_size(B, T, V), dev, stream)
+    _call("kda_draft_verify", dev, stream,
+          _ptr(target_probs, "target_probs", (B, T1, V), dt, dev),
+          None if draft_probs is None else _ptr(draft_probs, "draft_probs", (B, T, V), dt, dev),
+          _ptr(draft_tokens, "draft_tokens", (B, T), i32, dev),
+          _ptr(u, "u", (B, T1), torch.float32, dev),
+          None if n_draft is None else _ptr(n_draft, "n_draft", (B,), i32, dev),
+          _ptr(n_commit, "n_commit", (B,), i32, dev), _ptr(tokens, "tokens", (B, T1), i32, dev),
+          B, T, V, _kda._DTYPES[dt], wsp, wsz)
     return n_commit, tokens

@@ -30,6 +30,20 @@ __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirs
 __device__ __forceinline__ bool finite_bits(float x) {
     return (__builtin_bit_cast(uint32_t, x) & 0x7f800000u) != 0x7f800000u;
 }
+// x with 0 for its values that are not finite; odd is set if there is one.
+__device__ __forceinline__ bf16x8 only_finite(bf16x8 x, bool& odd) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4 w = __builtin_bit_cast(u32x4, x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t u = w[j];
+        const uint32_t lo = (u & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
+        const uint32_t hi = (u & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
+        odd |= (lo | hi) != 0;
+        w[j] = u & ~(lo | hi);
+    }
+    return __builtin_bit_cast(bf16x8, w);
+}
 __device__ __forceinline__ f32x4 mma4(float a, float b, f32x4 c) {
     // D(16x16) += A(16x4) B(4x16), fp32: lane l holds A[l%16][l/16], B[l/16][l%16]
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
@@ -253,11 +267,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, 
                 if (pos + (i * 64 + lane) / CH >= keys.end) vf[i] = bf16x8{};
         }
         // Positions that only some rows see: a value there that is not finite
-        // must not meet the weight 0 of the others in a product.
+        // must not meet the weight 0 of the others in a product. It counts 0
+        // here and is added below for the rows that see it.
         bool odd = false;
         if (pos + 32 > keys.all) {
-            for (int i = 0; i < VL; ++i)
-                for (int j = 0; j < 8; ++j) odd |= !finite_bits((float)vf[i][j]);
+            for (int i = 0; i < VL; ++i) vf[i] = only_finite(vf[i], odd);
             odd = __any(odd);
         }
         lds_fence_wave();                            // last step's reads of the stage are done
@@ -322,10 +336,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, 
                 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)x);
                 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(x + 16 * D));
             }
-            bf16x8 va = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-            if (odd)
-                for (int j = 0; j < 8; ++j)
-                    if (!finite_bits((float)va[j])) va[j] = (bf16)0.f;
+            const bf16x8 va = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
             for (int rt = 0; rt < RT; ++rt) acc[rt][b] = mma32(va, pf[rt], acc[rt][b]);
         }
         if (odd) {
@@ -629,15 +640,17 @@ __global__ __launch_bounds__(kAttnThreads, RW == 1 ? 2 : 1) void attn_tile_bf16(
         if (pos + 64 < keys.end) fetch(buf ^ 1, pos + 64, page);
         bool odd = false;
         if (edge) {
-            // rows that no row of the tile sees hold anything: they count 0
+            // Keys that no row of the tile sees hold anything: they count 0. Of the
+            // others a value that is not finite must not meet the weight 0 of the
+            // rows that do not see it: it counts 0 here and is added below.
             for (int i = 0; i < LD; ++i) {
                 bf16* v = vt + (16 * wave) * D + i * 512 + 8 * lane;
-                if (pos + 16 * wave + (i * 64 + lane) / CH >= keys.end) *(bf16x8*)v = bf16x8{};
-                const bf16x8 x = *(const bf16x8*)v;
-                for (int j = 0; j < 8; ++j) odd |= !finite_bits((float)x[j]);
+                bf16x8 x = *(const bf16x8*)v;
+                if (pos + 16 * wave + (i * 64 + lane) / CH >= keys.end) x = bf16x8{};
+                *(bf16x8*)v = only_finite(x, odd);
             }
-            if (lane == 0) odd_wave[wave] = 0;
-            if (__any(odd) && lane == 0) odd_wave[wave] = 1;
+            odd = __any(odd);
+            if (lane == 0) odd_wave[wave] = odd;
             __syncthreads();                         // the rows are cleared, the flags set
             odd = uniform(odd_wave[0] | odd_wave[1] | odd_wave[2] | odd_wave[3]);
             __syncthreads();                         // and read
@@ -698,16 +711,16 @@ __global__ __launch_bounds__(kAttnThreads, RW == 1 ? 2 : 1) void attn_tile_bf16(
                     x[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                         (lds_s16x4*)(vt + key * D + 8 * c + dv % 8));
                 }
-                bf16x8 va = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
-                if (odd)
-                    for (int j = 0; j < 8; ++j)
-                        if (!finite_bits((float)va[j])) va[j] = (bf16)0.f;
+                const bf16x8 va = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
                 for (int rw = 0; rw < RW; ++rw) acc[rw][b] = mma_big(va, pf[rw][ks], acc[rw][b]);
             }
         if (odd) {
             // the values left out above, for the rows that see them
             for (int y = 0; y < 64; ++y) {
-                if (pos + y >= keys.end || (missing >> (y / 16) & 1)) continue;
+                const int p = page_at(a, table, pos + (y & 48), keys.end);
+                if (p < 0 || pos + y >= keys.end) continue;
+                const bf16* gv = (const bf16*)a.vc +
+                    ((((long)p * a.Hkv + it.h) << a.page_shift) + ((pos + y) & row_mask)) * D;
                 for (int rw = 0; rw < RW; ++rw) {
                     float w = 0.f;
                     for (int u = 0; u < 2; ++u)
@@ -718,7 +731,7 @@ __global__ __launch_bounds__(kAttnThreads, RW == 1 ? 2 : 1) void attn_tile_bf16(
                     for (int b = 0; b < NB; ++b)
                         for (int i = 0; i < 16; ++i) {
                             const int dv = 32 * b + 8 * (i / 4) + 4 * half + i % 4;
-                            const float v = (float)vt[y * D + 8 * ((dv / 8) ^ (2 * (y & 3))) + dv % 8];
+                            const float v = (float)gv[dv];
                             if (sees && !finite_bits(v)) acc[rw][b][i] += w * v;
                         }
                 }
@@ -776,12 +789,16 @@ struct Joined {
 };
 
 template <typename T, int D>
-__global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit s) {
+__global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit s0, AttnSplit s1, int n0) {
     constexpr int kLanes = D / 4, kGroups = kAttnThreads / kLanes;
     __shared__ __align__(16) float lds_v[kGroups][D];
     __shared__ float lds_ml[kGroups][2];
     const int G = a.Hq / a.Hkv;
     const int group = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+    // the first n0 workgroups join the first launch's parts
+    const bool one = (int)blockIdx.x < n0;
+    const AttnSplit& s = one ? s0 : s1;
+    const unsigned block = one ? blockIdx.x : blockIdx.x - n0, blocks = one ? n0 : gridDim.x - n0;
     __shared__ AttnItem shared_item;
     __shared__ int shared_units;
     AttnSched<true> sched;
@@ -790,11 +807,11 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit 
         if (threadIdx.x == 0) shared_units = sched.items;
     }
     __syncthreads();
-    // an even share of the rows of all cut tiles, at most 2^12 tiles * 2^8
+    // an even share of the rows of all cut tiles, at most 2^11 tiles * 2^8
     const unsigned all = (unsigned)uniform(shared_units) << s.R_log2;
-    const unsigned share = (all + gridDim.x - 1) / gridDim.x;
-    const unsigned row_end = min(all, share * (blockIdx.x + 1));
-    for (unsigned r = share * blockIdx.x; r < row_end;) {
+    const unsigned share = (all + blocks - 1) / blocks;
+    const unsigned row_end = min(all, share * (block + 1));
+    for (unsigned r = share * block; r < row_end;) {
         const int x = (int)(r >> s.R_log2), row0 = (int)(r & (s.R - 1));
         __syncthreads();                             // the last item is read
         if (wave_id() == 0) sched.find(a, s, x, &shared_item);
@@ -873,22 +890,27 @@ struct Plan {
     bool tiles;            // the first is the tile kernel
     int RT;                // row groups of the stream kernel
     Launch l[2];
-    size_t bytes;          // workspace: the launches use it in turn
+    size_t bytes;          // workspace
 };
-Launch launch_of(long T, long B, long G, long Hkv, int R, int unit, int target_log2) {
+Launch launch_of(long T, long B, long G, long Hkv, int R, int unit, int most_log2,
+                 int few_log2, int max_rows) {
     Launch l{};
     l.split.R = R;
     l.split.R_log2 = __builtin_ctz((unsigned)R);
     l.split.min_rows = 1;
-    l.split.max_rows = INT32_MAX;
+    l.split.max_rows = max_rows;
     l.split.unit = unit;
-    l.split.target_log2 = target_log2;
-    const long target = 1l << target_log2, tiles = attn_max_tiles(T, B, G, Hkv, R);
+    l.split.most_log2 = most_log2;
+    l.split.few_log2 = few_log2;
+    // requests of no more rows than a tile are a tile each
+    const long target = 1l << most_log2;
+    const long tiles = max_rows <= R ? (B < T ? B : T) * Hkv : attn_max_tiles(T, B, G, Hkv, R);
     l.items = attn_max_items(tiles, target);
     l.split.slots = (int)attn_max_slots(target);
-    // the joining's share of a row or more each
+    // the joining's: a row or more each (2048 workgroups: 7 to 9 us more where
+    // there is little to join, no less where there is much)
     const long rows = (tiles < target ? tiles : target) * R;
-    l.joins = rows < 2048 ? rows : 2048;
+    l.joins = rows < 1024 ? rows : 1024;
     return l;
 }
 Plan plan_of(int T, int B, int Hq, int Hkv, int d, int max_new, bool bf16_io) {
@@ -897,21 +919,18 @@ Plan plan_of(int T, int B, int Hq, int Hkv, int d, int max_new, bool bf16_io) {
     p.tiles = bf16_io && d >= 64 && most > kStreamRows;
     p.RT = most <= 16 ? 1 : 2;
     if (p.tiles) {
-        p.l[p.n] = launch_of(T, B, G, Hkv, 128 * kTileGroups, 64, 9);
+        p.l[p.n] = launch_of(T, B, G, Hkv, 128 * kTileGroups, 64, 9, 9, INT32_MAX);
         p.l[p.n].split.min_rows = kStreamRows + 1;
         ++p.n;
     }
     if (!p.tiles || B > 1) {
-        p.l[p.n] = launch_of(T, B, G, Hkv, 16 * p.RT, 128, 11);
-        if (p.tiles) p.l[p.n].split.max_rows = kStreamRows;
+        p.l[p.n] = launch_of(T, B, G, Hkv, 16 * p.RT, 128, 11, 8, p.tiles ? kStreamRows : INT32_MAX);
         ++p.n;
     }
     // a single request is the tile kernel's whatever its length
     if (p.tiles && B == 1) p.l[0].split.min_rows = 1;
-    for (int i = 0; i < p.n; ++i) {
-        const size_t x = (size_t)p.l[i].split.slots * p.l[i].split.R * (d + 2) * sizeof(float);
-        if (x > p.bytes) p.bytes = x;
-    }
+    for (int i = 0; i < p.n; ++i)
+        p.bytes += (size_t)p.l[i].split.slots * p.l[i].split.R * (d + 2) * sizeof(float);
     return p;
 }
 
@@ -940,10 +959,11 @@ hipError_t launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
         } else {
             launch_stream<D>(a, p, l, st);
         }
-        const unsigned n = (unsigned)l.joins;
-        if (a.bf16_io) attn_join<bf16, D><<<n, kAttnThreads, 0, st>>>(a, l.split);
-        else attn_join<float, D><<<n, kAttnThreads, 0, st>>>(a, l.split);
     }
+    const AttnSplit &s0 = p.l[0].split, &s1 = p.l[p.n - 1].split;
+    const int n0 = (int)p.l[0].joins, n = n0 + (p.n > 1 ? (int)p.l[1].joins : 0);
+    if (a.bf16_io) attn_join<bf16, D><<<(unsigned)n, kAttnThreads, 0, st>>>(a, s0, s1, n0);
+    else attn_join<float, D><<<(unsigned)n, kAttnThreads, 0, st>>>(a, s0, s1, n0);
     return hipGetLastError();
 }
 
@@ -955,10 +975,12 @@ size_t attn_paged_ws(int T, int B, int Hq, int Hkv, int d, int max_new, bool bf1
 
 hipError_t launch_attn_paged(const AttnArgs& a, void* ws, hipStream_t st) {
     Plan p = plan_of(a.T, a.B, a.Hq, a.Hkv, a.d, a.max_new, a.bf16_io);
+    float* at = (float*)ws;
     for (int i = 0; i < p.n; ++i) {
         AttnSplit& s = p.l[i].split;
-        s.ml = (float*)ws;
+        s.ml = at;
         s.acc = s.ml + (size_t)s.slots * s.R * 2;
+        at = s.acc + (size_t)s.slots * s.R * a.d;
     }
     switch (a.d) {
         case 16: return launch<16>(a, p, st);

@@ -3,8 +3,8 @@
 // The n new tokens of a request and the G query heads of a KV head form n * G
 // rows (row r: token r / G, head r % G), cut into tiles of R rows. A tile's
 // keys are cut into parts of C keys, C such that all tiles of the call make
-// about 2^target_log2 parts: one part per tile when there are tiles enough,
-// many when few long requests have to fill the card. Lengths are on the
+// some hundreds of parts: one part per tile when there are tiles enough, many
+// when few long requests have to fill the card. Lengths are on the
 // device, so the first wave of each workgroup reads them, four requests a
 // lane, sums the work and finds its part in the prefix sums, in registers:
 // about 300 instructions up to 256 requests, where a kernel that writes the
@@ -19,6 +19,11 @@ namespace kda {
 namespace {
 
 constexpr int kAttnThreads = 256;
+// Starting a part costs about as much as 1024 of its keys: more parts than
+// there is room for on the card balance uneven lengths, but not below this
+// length (a batch of 480 short fp32 tiles: 29 us with 2048 parts, see the
+// kernels for the rest).
+constexpr int kLongPart = 1024;
 
 // What a launch works on, besides AttnArgs.
 struct AttnSplit {
@@ -26,7 +31,8 @@ struct AttnSplit {
     int min_rows;       // only requests of at least min_rows rows ...
     int max_rows;       // ... and at most max_rows of them
     int unit;           // granularity and least length of a part, a power of two
-    int target_log2;    // parts wanted over the whole call: 2^target_log2
+    int most_log2;      // parts over the whole call: at most about 2^most_log2 ...
+    int few_log2;       // ... and as few as 2^few_log2 rather than parts below kLongPart
     int slots;          // partial results that the workspace holds
     float* ml;          // [slots][R][2]: running maximum (log2 domain), sum
     float* acc;         // [slots][R][d]: unnormalised rows
@@ -171,8 +177,10 @@ struct AttnSched {
             b.load(a, s, base);
             cost += b.cost();
         }
-        const float want = wave_sum_uniform(cost) * (float)a.Hkv *
-                           __builtin_bit_cast(float, (127 - s.target_log2) << 23);
+        const float total = wave_sum_uniform(cost) * (float)a.Hkv;
+        const float most = total * __builtin_bit_cast(float, (127 - s.most_log2) << 23);
+        const float few = total * __builtin_bit_cast(float, (127 - s.few_log2) << 23);
+        const float want = fmaxf(most, fminf(few, (float)kLongPart));
         // a part covers at most all positions
         C = __builtin_amdgcn_readfirstlane(((int)fminf(want, 1073741824.f) & ~(s.unit - 1)) + s.unit);
         first.split(a, C);

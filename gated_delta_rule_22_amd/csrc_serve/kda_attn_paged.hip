@@ -20,10 +20,7 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 constexpr int kKeepAll = 1 << 30;
-#ifndef KTG
-#define KTG 1
-#endif
-constexpr int kTileGroups = KTG;
+constexpr int kTileRows = 128;
 
 __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -152,6 +149,23 @@ __device__ __forceinline__ int page_at(const AttnArgs& a, const_int* table, int 
     return (unsigned)p < (unsigned)a.pool ? p : -1;
 }
 
+// Which 16-byte piece of a row of D values LDS holds in place of piece c, so
+// that the reads of 16 lanes (16 bytes each) or 32 (8 bytes) cover the 64
+// banks once. Rows are 2 D bytes, 256 / (2 D) of them cover the banks.
+// K: 16 lanes read piece c of 16 keys.
+template <int D> __device__ __forceinline__ int k_piece(int key, int c) {
+    return D >= 128 ? c ^ (key & 15) : c ^ (key >> 1 & 7);
+}
+// V, transposing reads: 32 lanes take 64 bytes of four consecutive keys, ...
+template <int D> __device__ __forceinline__ int v_piece4(int key, int c) {
+    return D >= 128 ? c ^ 4 * (key & 3) : c ^ 4 * (key >> 1 & 1);
+}
+// ... or 32 bytes of eight.
+template <int D> __device__ __forceinline__ int v_piece8(int key, int c) {
+    return D >= 128 ? c ^ 2 * (key & 7) : D == 64 ? c ^ 2 * (key >> 1 & 3)
+         : D == 32 ? c ^ 2 * (key >> 2 & 1) : c;
+}
+
 // The running maximum, sum and rows of 16 RT rows in one wave. Lane l holds
 // row l % 16 of each group of 16 throughout; l is a sum over the lane's own
 // keys until finish().
@@ -277,10 +291,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, 
         lds_fence_wave();                            // last step's reads of the stage are done
         for (int i = 0; i < VL; ++i) {
             const int x = i * 64 + lane, key = x / CH, c = x % CH;
-            // a 16-lane transposing read takes 32 bytes of four rows: rows of
-            // 128 bytes and more put them 32 bytes apart
-            const int sw = D >= 64 ? c ^ (2 * (key & 3)) : c;
-            *(bf16x8*)(stage + key * D + 8 * sw) = vf[i];
+            *(bf16x8*)(stage + key * D + 8 * v_piece8<D>(key, c)) = vf[i];
         }
         const int p0 = page[0], p1 = page[1];
         page[0] = page_next[0];
@@ -331,8 +342,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, 
             s16x4 lo, hi;
             {
                 const int key = 4 * g4 + c16 / 4, c = 2 * b + (c16 & 3) / 2;
-                const int sw = D >= 64 ? c ^ (2 * (key & 3)) : c;
-                const bf16* x = stage + key * D + 8 * sw + 4 * (c16 & 1);
+                const bf16* x = stage + key * D + 8 * v_piece8<D>(key, c) + 4 * (c16 & 1);
                 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)x);
                 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(x + 16 * D));
             }
@@ -541,7 +551,6 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_f32(AttnArgs a, A
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
-typedef const __attribute__((address_space(1))) void glb_void;
 
 // D(32x32) += A(32x16) B(16x32): lane l holds A[l%32][8(l/32)..+7],
 // B[8(l/32)..+7][l%32], D[8(i/4) + 4(l/32) + i%4][l%32] in element i.
@@ -550,23 +559,37 @@ __device__ __forceinline__ f32x16 mma_big(bf16x8 a, bf16x8 b, f32x16 c) {
 }
 __device__ __forceinline__ float max_halves(float x) { return fmaxf(x, __shfl_xor(x, 32)); }
 
-// Prompts: tiles of 128 RW rows, 32 RW per wave, against 64 keys at a time
-// that all waves share in LDS, double buffered. What bounds it is the matrix
-// cores, 4 D flops per row and key, and next to them the exponentials.
+// 16 bytes a lane from base + off (bytes, per lane) to LDS at the wave's
+// address `to`, in the order of the lanes. As inline assembly, because the
+// compiler otherwise waits for all of them before it reads any LDS with a
+// transposing load; there is no result register, and the kernel waits itself.
+__device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, const void* base) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 ::"s"(to), "v"(off), "s"(base) : "memory");
+}
+
+// Prompts: tiles of 128 rows, 32 per wave, against 64 keys at a time that all
+// waves share in LDS. What bounds it is the matrix cores, 4 D flops per row
+// and key, the LDS reads that feed them (each wave reads all 64 keys and
+// values for its 32 rows: 32 cycles a product, as long as the product takes),
+// and the exponentials.
 //
 // As above S^T = K Q^T and O^T += V^T P^T, with the 32x32x16 product: the
 // scores of row l % 32 stay in lanes l and l + 32 and are the second operand
-// of the next product as they are. K and V go from memory to LDS directly, 16
-// bytes a lane in the lanes' order; which 16 bytes of the row each lane
-// fetches is permuted, so that the reads meet no bank twice: K's pieces by
-// the key's low 3 bits (8 lanes read the same piece of 8 keys), V's pairs of
-// pieces by its low 2 (a 16-lane transposing read takes 32 bytes of 4 keys).
-template <int D, int RW>
-__global__ __launch_bounds__(kAttnThreads, RW == 1 ? 2 : 1) void attn_tile_bf16(AttnArgs a,
-                                                                               AttnSplit s) {
+// of the next product as they are. The scores of the next 64 keys are made
+// while the exponentials of these run, so that the matrix cores have work in
+// both; K is therefore fetched two steps ahead and V one, two buffers each.
+//
+// K and V go from memory to LDS directly, 16 bytes a lane in the lanes' order;
+// which 16 bytes of the row each lane fetches is permuted (k_piece, v_piece4):
+// with 8 lanes' worth of banks in mind instead of 16, half of the LDS cycles
+// were conflicts.
+template <int D>
+__global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_tile_bf16(AttnArgs a, AttnSplit s) {
     constexpr int KS = D / 16, NB = D / 32, CH = D / 8, LD = 16 * CH / 64;
-    __shared__ __align__(128) bf16 kbuf[2][64 * D], vbuf[2][64 * D];
-    __shared__ int gap_wave[2][4], odd_wave[4];
+    constexpr int kTile = 64 * D;                    // of K or V
+    __shared__ __align__(128) bf16 kbuf[2 * kTile], vbuf[2 * kTile];
+    __shared__ int gap_wave[4][4], odd_wave[4];
     __shared__ AttnItem shared_item;
     const AttnItem it = attn_item(a, s, (int)blockIdx.x, shared_item);
     if (!it.found) return;
@@ -577,69 +600,102 @@ __global__ __launch_bounds__(kAttnThreads, RW == 1 ? 2 : 1) void attn_tile_bf16(
     const float scale = a.scale * kLog2e;
     const int row_mask = (1 << a.page_shift) - 1;
 
-    bf16x8 qf[RW][KS];
-    int limit[RW];
-    RowAt at[RW];
-    for (int rw = 0; rw < RW; ++rw) {
-        at[rw] = row_at(a, it, G, it.tile * s.R + (wave * RW + rw) * 32 + c32);
-        limit[rw] = at[rw].in ? (int)min((long)it.kept + at[rw].t, (long)kKeepAll) : -1;
-        const bf16* q = (const bf16*)a.q + at[rw].q * D + 8 * half;
-        for (int k = 0; k < KS; ++k) {
-            bf16x8 z = {};
-            if (at[rw].in) z = *(const bf16x8*)(q + 16 * k);
-            qf[rw][k] = z;
-        }
+    bf16x8 qf[KS];
+    const RowAt at = row_at(a, it, G, it.tile * s.R + wave * 32 + c32);
+    const int limit = at.in ? (int)min((long)it.kept + at.t, (long)kKeepAll) : -1;
+    for (int k = 0; k < KS; ++k) {
+        bf16x8 z = {};
+        if (at.in) z = *(const bf16x8*)((const bf16*)a.q + at.q * D + 8 * half + 16 * k);
+        qf[k] = z;
     }
-    float m[RW], l[RW];
-    f32x16 acc[RW][NB];
-    for (int rw = 0; rw < RW; ++rw) {
-        m[rw] = -INFINITY;
-        l[rw] = 0.f;
-        for (int b = 0; b < NB; ++b) acc[rw][b] = f32x16{};
-    }
+    float m = -INFINITY, l = 0.f;
+    f32x16 acc[NB];
+    for (int b = 0; b < NB; ++b) acc[b] = f32x16{};
 
-    // This wave's 16 keys of the tile at pos, from page p (-1: zeros).
-    auto fetch = [&](int buf, int pos, int p) {
-        bf16* k = kbuf[buf] + 16 * wave * D;
-        bf16* v = vbuf[buf] + 16 * wave * D;
+    // where the lane's 16 bytes of the wave's 16 keys come from
+    uint32_t koff[LD], voff[LD];
+    for (int i = 0; i < LD; ++i) {
+        const int x = i * 64 + lane, r = x / CH, c = x % CH;
+        koff[i] = 2 * (r * D + 8 * k_piece<D>(r, c));
+        voff[i] = 2 * (r * D + 8 * v_piece4<D>(r, c));
+    }
+    auto page_of = [&](int pos) { return page_at(a, table, pos + 16 * wave, keys.end); };
+    // This wave's 16 keys (values) of the step at pos, from page p; zeros where
+    // there is none.
+    auto fetch = [&](const void* cache, bf16* buf, const uint32_t* off, int pos, int p) {
+        bf16* to = buf + 16 * wave * D;
         if (p >= 0) {
             const long row = (((long)p * a.Hkv + it.h) << a.page_shift) + ((pos + 16 * wave) & row_mask);
-            const bf16* gk = (const bf16*)a.kc + row * D;
-            const bf16* gv = (const bf16*)a.vc + row * D;
-            for (int i = 0; i < LD; ++i) {
-                const int x = i * 64 + lane, r = x / CH, c = x % CH;
-                __builtin_amdgcn_global_load_lds((glb_void*)(gk + r * D + 8 * (c ^ (r & 7))),
-                                                 (lds_void*)(k + i * 512), 16, 0, 0);
-                __builtin_amdgcn_global_load_lds((glb_void*)(gv + r * D + 8 * (c ^ (2 * (r & 3)))),
-                                                 (lds_void*)(v + i * 512), 16, 0, 0);
-            }
+            const bf16* from = (const bf16*)cache + row * D;
+            const uint32_t lds = uniform((int)(uint32_t)(uintptr_t)(lds_void*)to);
+            for (int i = 0; i < LD; ++i) load_to_lds(lds + i * 1024, off[i], from);
         } else {
-            for (int i = 0; i < LD; ++i) {
-                *(bf16x8*)(k + i * 512 + 8 * lane) = bf16x8{};
-                *(bf16x8*)(v + i * 512 + 8 * lane) = bf16x8{};
+            for (int i = 0; i < LD; ++i) *(bf16x8*)(to + i * 512 + 8 * lane) = bf16x8{};
+        }
+    };
+    // Scores of the step whose keys are in kt.
+    auto scores = [&](const bf16* kt, f32x16 (&st)[2]) {
+        for (int u = 0; u < 2; ++u) {
+            st[u] = f32x16{};
+            for (int k = 0; k < KS; ++k) {
+                const int c = k_piece<D>(c32, 2 * k + half);
+                const bf16x8 kf = *(const bf16x8*)(kt + (32 * u + c32) * D + 8 * c);
+                st[u] = mma_big(kf, qf[k], st[u]);
             }
         }
     };
-    auto page_of = [&](int pos) { return page_at(a, table, pos + 16 * wave, keys.end); };
+    auto missing_of = [&](int step) {
+        int missing = 0;
+        for (int w = 0; w < 4; ++w) missing |= uniform(gap_wave[step & 3][w]) << w;
+        return missing;
+    };
+    // Masks the scores of the step at pos and moves the reference m. It may
+    // stay behind the maximum by up to 8 in the log2 domain: weights up to 2^8
+    // lose nothing, and the rows are rescaled a few times instead of with
+    // every new maximum.
+    auto settle = [&](f32x16 (&st)[2], int pos, int missing) {
+        if (pos + 64 > keys.all || missing) {
+            for (int u = 0; u < 2; ++u)
+                for (int i = 0; i < 16; ++i) {
+                    const int y = 32 * u + 8 * (i / 4) + 4 * half + i % 4;
+                    if (pos + y > limit || pos + y >= keys.end || (missing >> (y / 16) & 1))
+                        st[u][i] = -INFINITY;
+                }
+        }
+        float mx = -INFINITY;
+        for (int u = 0; u < 2; ++u)
+            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, st[u][i]);
+        mx = max_halves(mx) * scale;
+        if (__any(mx > m + 8.f)) {
+            const float mn = fmaxf(m, mx);
+            const float c = mn == -INFINITY ? 1.f : exp2_f(m - mn);
+            m = mn;
+            l *= c;
+            for (int b = 0; b < NB; ++b) acc[b] *= c;
+        }
+    };
 
-    int buf = 0, page = page_of(keys.begin), page_next = page_of(keys.begin + 64);
-    if (keys.begin < keys.end) fetch(0, keys.begin, page);
-    for (int pos = keys.begin; pos < keys.end; pos += 64, buf ^= 1) {
-        // missing pages are known to the wave that fetches them only; two sets
-        // of flags, since a wave may set the next ones while another reads these
-        if (lane == 0) gap_wave[buf][wave] = page < 0;
+    // One step: st holds the settled scores of the keys at pos (the step-th of
+    // the part), next receives those of the keys behind them.
+    int page_v = 0;                      // of K two steps ahead, V one
+    auto advance = [&](int pos, int step) {
+        const int buf = step & 1;
+        const bf16* kt = kbuf + buf * kTile;
+        f32x16 st[2];
+        bf16* vt = vbuf + buf * kTile;
+        // pages missing in the keys two steps ahead: known to the wave that
+        // fetches them. Four sets of flags: a wave sets those of one step while
+        // another still reads an older one's.
+        if (lane == 0) gap_wave[(step + 1) & 3][wave] = page_v < 0;
         __builtin_amdgcn_s_waitcnt(0x0f70);          // vmcnt(0): this wave's part has landed
         __syncthreads();
-        int missing = 0;
-        for (int w = 0; w < 4; ++w) missing |= uniform(gap_wave[buf][w]) << w;
-        const bool edge = pos + 64 > keys.all || missing;
-        const bf16* kt = kbuf[buf];
-        bf16* vt = vbuf[buf];
-        page = page_next;
-        page_next = page_of(pos + 128);
-        if (pos + 64 < keys.end) fetch(buf ^ 1, pos + 64, page);
+        const bool more = pos + 64 < keys.end;
+        if (more) fetch(a.kc, kbuf + (buf ^ 1) * kTile, koff, pos + 64, page_v);
+        if (more) fetch(a.vc, vbuf + (buf ^ 1) * kTile, voff, pos + 64, page_v);
+        page_v = page_of(pos + 128);
         bool odd = false;
-        if (edge) {
+        const int missing = missing_of(step);
+        if (pos + 64 > keys.all || missing) {
             // Keys that no row of the tile sees hold anything: they count 0. Of the
             // others a value that is not finite must not meet the weight 0 of the
             // rows that do not see it: it counts 0 here and is added below.
@@ -651,68 +707,37 @@ __global__ __launch_bounds__(kAttnThreads, RW == 1 ? 2 : 1) void attn_tile_bf16(
             }
             odd = __any(odd);
             if (lane == 0) odd_wave[wave] = odd;
-            __syncthreads();                         // the rows are cleared, the flags set
+            __syncthreads();                         // the values are cleared, the flags set
             odd = uniform(odd_wave[0] | odd_wave[1] | odd_wave[2] | odd_wave[3]);
             __syncthreads();                         // and read
         }
-
-        f32x16 st[RW][2];
-        for (int u = 0; u < 2; ++u) {
-            for (int rw = 0; rw < RW; ++rw) st[rw][u] = f32x16{};
-            for (int k = 0; k < KS; ++k) {
-                const int c = (2 * k + half) ^ (c32 & 7);
-                const bf16x8 kf = *(const bf16x8*)(kt + (32 * u + c32) * D + 8 * c);
-                for (int rw = 0; rw < RW; ++rw) st[rw][u] = mma_big(kf, qf[rw][k], st[rw][u]);
+        scores(kt, st);
+        settle(st, pos, missing);
+        const float mu = m == -INFINITY ? 0.f : m;
+        bf16x8 pf[4];
+        float sum = 0.f;
+        for (int u = 0; u < 2; ++u)
+            for (int i = 0; i < 16; ++i) {
+                const float p = exp2_f(__builtin_fmaf(st[u][i], scale, -mu));
+                sum += p;
+                st[u][i] = p;
             }
-        }
-        bf16x8 pf[RW][4];
-        for (int rw = 0; rw < RW; ++rw) {
-            if (edge) {
-                for (int u = 0; u < 2; ++u)
-                    for (int i = 0; i < 16; ++i) {
-                        const int y = 32 * u + 8 * (i / 4) + 4 * half + i % 4;
-                        if (pos + y > limit[rw] || pos + y >= keys.end || (missing >> (y / 16) & 1))
-                            st[rw][u][i] = -INFINITY;
-                    }
-            }
-            float mx = -INFINITY;
-            for (int u = 0; u < 2; ++u)
-                for (int i = 0; i < 16; ++i) mx = fmaxf(mx, st[rw][u][i]);
-            mx = max_halves(mx) * scale;
-            // The reference m may stay behind the maximum by up to 8 in the
-            // log2 domain: weights up to 2^8 lose nothing, and the rows are
-            // rescaled a few times instead of with every new maximum.
-            if (__any(mx > m[rw] + 8.f)) {
-                const float mn = fmaxf(m[rw], mx);
-                const float c = mn == -INFINITY ? 1.f : exp2_f(m[rw] - mn);
-                m[rw] = mn;
-                l[rw] *= c;
-                for (int b = 0; b < NB; ++b) acc[rw][b] *= c;
-            }
-            const float mu = m[rw] == -INFINITY ? 0.f : m[rw];
-            float sum = 0.f;
-            for (int u = 0; u < 2; ++u)
-                for (int i = 0; i < 16; ++i) {
-                    const float p = exp2_f(__builtin_fmaf(st[rw][u][i], scale, -mu));
-                    sum += p;
-                    st[rw][u][i] = p;
-                }
-            l[rw] += sum;
-            for (int ks = 0; ks < 4; ++ks)
-                for (int j = 0; j < 8; ++j) pf[rw][ks][j] = (bf16)st[rw][ks / 2][8 * (ks % 2) + j];
-        }
+        l += sum;
+        // the weights are rounded to bf16 for the matrix cores; l sums them unrounded
+        for (int ks = 0; ks < 4; ++ks)
+            for (int j = 0; j < 8; ++j) pf[ks][j] = (bf16)st[ks / 2][8 * (ks % 2) + j];
         for (int ks = 0; ks < 4; ++ks)
             for (int b = 0; b < NB; ++b) {
                 s16x4 x[2];
                 for (int j = 0; j < 2; ++j) {
                     const int key = 16 * ks + 8 * j + 4 * half + (lane & 15) / 4;
                     const int dv = 32 * b + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-                    const int c = (dv / 8) ^ (2 * (key & 3));
+                    const int c = v_piece4<D>(key, dv / 8);
                     x[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                         (lds_s16x4*)(vt + key * D + 8 * c + dv % 8));
                 }
                 const bf16x8 va = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
-                for (int rw = 0; rw < RW; ++rw) acc[rw][b] = mma_big(va, pf[rw][ks], acc[rw][b]);
+                acc[b] = mma_big(va, pf[ks], acc[b]);
             }
         if (odd) {
             // the values left out above, for the rows that see them
@@ -721,52 +746,56 @@ __global__ __launch_bounds__(kAttnThreads, RW == 1 ? 2 : 1) void attn_tile_bf16(
                 if (p < 0 || pos + y >= keys.end) continue;
                 const bf16* gv = (const bf16*)a.vc +
                     ((((long)p * a.Hkv + it.h) << a.page_shift) + ((pos + y) & row_mask)) * D;
-                for (int rw = 0; rw < RW; ++rw) {
-                    float w = 0.f;
-                    for (int u = 0; u < 2; ++u)
-                        for (int i = 0; i < 16; ++i)
-                            if (y / 32 == u && (y & 31) / 8 == i / 4 && y % 4 == i % 4) w = st[rw][u][i];
-                    w = __shfl(w, c32 + 32 * ((y / 4) & 1));
-                    const bool sees = pos + y <= limit[rw];
-                    for (int b = 0; b < NB; ++b)
-                        for (int i = 0; i < 16; ++i) {
-                            const int dv = 32 * b + 8 * (i / 4) + 4 * half + i % 4;
-                            const float v = (float)gv[dv];
-                            if (sees && !finite_bits(v)) acc[rw][b][i] += w * v;
-                        }
-                }
+                float w = 0.f;
+                for (int u = 0; u < 2; ++u)
+                    for (int i = 0; i < 16; ++i)
+                        if (y / 32 == u && (y & 31) / 8 == i / 4 && y % 4 == i % 4) w = st[u][i];
+                w = __shfl(w, c32 + 32 * ((y / 4) & 1));
+                const bool sees = pos + y <= limit;
+                for (int b = 0; b < NB; ++b)
+                    for (int i = 0; i < 16; ++i) {
+                        const float v = (float)gv[32 * b + 8 * (i / 4) + 4 * half + i % 4];
+                        if (sees && !finite_bits(v)) acc[b][i] += w * v;
+                    }
             }
         }
+    };
+
+    if (keys.begin < keys.end) {
+        const int p0 = page_of(keys.begin);
+        page_v = page_of(keys.begin + 64);
+        if (lane == 0) gap_wave[0][wave] = p0 < 0;
+        fetch(a.kc, kbuf, koff, keys.begin, p0);
+        fetch(a.vc, vbuf, voff, keys.begin, p0);
+        for (int pos = keys.begin, step = 0; pos < keys.end; pos += 64, ++step) advance(pos, step);
     }
 
-    for (int rw = 0; rw < RW; ++rw) {
-        const float sum = l[rw] + __shfl_xor(l[rw], 32);
-        const int row = (wave * RW + rw) * 32 + c32;
-        if (it.parts > 1) {
-            const long slot = (long)it.slot + ((long)it.part * it.tiles + it.tile) * a.Hkv + it.h;
-            if ((unsigned long)slot >= (unsigned long)s.slots) return;
-            float* x = s.acc + (slot * s.R + row) * D;
-            for (int b = 0; b < NB; ++b)
-                for (int i = 0; i < 16; i += 4)
-                    *(f32x4*)(x + 32 * b + 2 * i + 4 * half) =
-                        f32x4{acc[rw][b][i], acc[rw][b][i + 1], acc[rw][b][i + 2], acc[rw][b][i + 3]};
-            if (half == 0) {
-                s.ml[(slot * s.R + row) * 2] = m[rw];
-                s.ml[(slot * s.R + row) * 2 + 1] = sum;
-            }
-            continue;
-        }
-        if (!at[rw].in) continue;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        bf16* o = (bf16*)a.o + at[rw].q * D;
+    const float sum = l + __shfl_xor(l, 32);
+    const int row = wave * 32 + c32;
+    if (it.parts > 1) {
+        const long slot = (long)it.slot + ((long)it.part * it.tiles + it.tile) * a.Hkv + it.h;
+        if ((unsigned long)slot >= (unsigned long)s.slots) return;   // only where offsets decrease
+        float* x = s.acc + (slot * s.R + row) * D;
         for (int b = 0; b < NB; ++b)
-            for (int i = 0; i < 16; i += 4) {
-                bf16x4 x;
-                for (int j = 0; j < 4; ++j) x[j] = (bf16)(acc[rw][b][i + j] * inv);
-                *(bf16x4*)(o + 32 * b + 2 * i + 4 * half) = x;
-            }
-        if (a.lse && half == 0) a.lse[at[rw].q] = sum == 0.f ? -INFINITY : (m[rw] + __log2f(sum)) * kLn2;
+            for (int i = 0; i < 16; i += 4)
+                *(f32x4*)(x + 32 * b + 2 * i + 4 * half) =
+                    f32x4{acc[b][i], acc[b][i + 1], acc[b][i + 2], acc[b][i + 3]};
+        if (half == 0) {
+            s.ml[(slot * s.R + row) * 2] = m;
+            s.ml[(slot * s.R + row) * 2 + 1] = sum;
+        }
+        return;
     }
+    if (!at.in) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    bf16* o = (bf16*)a.o + at.q * D;
+    for (int b = 0; b < NB; ++b)
+        for (int i = 0; i < 16; i += 4) {
+            bf16x4 x;
+            for (int j = 0; j < 4; ++j) x[j] = (bf16)(acc[b][i + j] * inv);
+            *(bf16x4*)(o + 32 * b + 2 * i + 4 * half) = x;
+        }
+    if (a.lse && half == 0) a.lse[at.q] = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * kLn2;
 }
 
 // Joins the parts of tiles that were cut, rows shared evenly by the workgroups.
@@ -919,7 +948,7 @@ Plan plan_of(int T, int B, int Hq, int Hkv, int d, int max_new, bool bf16_io) {
     p.tiles = bf16_io && d >= 64 && most > kStreamRows;
     p.RT = most <= 16 ? 1 : 2;
     if (p.tiles) {
-        p.l[p.n] = launch_of(T, B, G, Hkv, 128 * kTileGroups, 64, 9, 9, INT32_MAX);
+        p.l[p.n] = launch_of(T, B, G, Hkv, kTileRows, 64, 9, 9, INT32_MAX);
         p.l[p.n].split.min_rows = kStreamRows + 1;
         ++p.n;
     }
@@ -947,7 +976,7 @@ void launch_stream(const AttnArgs& a, const Plan& p, const Launch& l, hipStream_
 }
 template <int D>
 void launch_tile(const AttnArgs& a, const Launch& l, hipStream_t st) {
-    attn_tile_bf16<D, kTileGroups><<<(unsigned)l.items, kAttnThreads, 0, st>>>(a, l.split);
+    attn_tile_bf16<D><<<(unsigned)l.items, kAttnThreads, 0, st>>>(a, l.split);
 }
 
 template <int D>

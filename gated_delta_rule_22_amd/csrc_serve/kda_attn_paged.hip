@@ -635,14 +635,27 @@ __global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_tile_bf16(
     };
     // Scores of the step whose keys are in kt.
     auto scores = [&](const bf16* kt, f32x16 (&st)[2]) {
-        for (int u = 0; u < 2; ++u) {
-            st[u] = f32x16{};
-            for (int k = 0; k < KS; ++k) {
-                const int c = k_piece<D>(c32, 2 * k + half);
-                const bf16x8 kf = *(const bf16x8*)(kt + (32 * u + c32) * D + 8 * c);
-                st[u] = mma_big(kf, qf[k], st[u]);
-            }
+        bf16x8 kf[2][KS];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+                kf[u][k] = *(const bf16x8*)(kt + (32 * u + c32) * D + 8 * k_piece<D>(c32, 2 * k + half));
+        st[0] = f32x16{};
+        st[1] = f32x16{};
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int k = 0; k < KS; ++k) st[u] = mma_big(kf[u][k], qf[k], st[u]);
+        // the first half's reads, then a read behind every product: left to
+        // itself the compiler reads into one register and waits each time
+        __builtin_amdgcn_sched_group_barrier(0x100, KS, 0);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
+        __builtin_amdgcn_sched_group_barrier(0x008, KS, 0);
     };
     auto missing_of = [&](int step) {
         int missing = 0;

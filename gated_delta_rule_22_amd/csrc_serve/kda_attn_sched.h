@@ -31,8 +31,9 @@ struct AttnSplit {
     int min_rows;       // only requests of at least min_rows rows ...
     int max_rows;       // ... and at most max_rows of them
     int unit;           // granularity and least length of a part, a power of two
-    int most_log2;      // parts over the whole call: at most about 2^most_log2 ...
-    int few_log2;       // ... and as few as 2^few_log2 rather than parts below kLongPart
+    int most_log2;      // parts over the whole call: about as many as tiles, but not
+    int some_log2;      // more than 2^most_log2, not fewer than 2^some_log2, and as few
+    int few_log2;       // as 2^few_log2 rather than parts shorter than kLongPart
     int slots;          // partial results that the workspace holds
     float* ml;          // [slots][R][2]: running maximum (log2 domain), sum
     float* acc;         // [slots][R][d]: unnormalised rows
@@ -99,6 +100,7 @@ struct AttnBlock {
         r2 = attn_req(a, s, i + 2 <= last, u2, u3, k2);
         r3 = attn_req(a, s, i + 3 <= last, u3, u4, k3);
     }
+    __device__ int tiles() const { return r0.tiles + r1.tiles + (r2.tiles + r3.tiles); }
     __device__ float cost() const {
         return (float)r0.tiles * (float)r0.kv + (float)r1.tiles * (float)r1.kv +
                ((float)r2.tiles * (float)r2.kv + (float)r3.tiles * (float)r3.kv);
@@ -171,14 +173,17 @@ struct AttnSched {
 
     __device__ void init(const AttnArgs& a, const AttnSplit& s) {
         first.load(a, s, 0);
-        float cost = first.cost();
+        float cost = first.cost(), tiles = (float)first.tiles();
         for (int base = 256; base < a.B; base += 256) {
             AttnBlock<UNITS> b;
             b.load(a, s, base);
             cost += b.cost();
+            tiles += (float)b.tiles();
         }
         const float total = wave_sum_uniform(cost) * (float)a.Hkv;
-        const float most = total * __builtin_bit_cast(float, (127 - s.most_log2) << 23);
+        tiles = wave_sum_uniform(tiles) * (float)a.Hkv;
+        const float parts = fminf(fmaxf(tiles, (float)(1 << s.some_log2)), (float)(1 << s.most_log2));
+        const float most = total / parts;
         const float few = total * __builtin_bit_cast(float, (127 - s.few_log2) << 23);
         const float want = fmaxf(most, fminf(few, (float)kLongPart));
         // a part covers at most all positions

@@ -178,24 +178,27 @@ template <int D> __device__ __forceinline__ int v_piece8(int key, int c) {
 // row against keys 16 sub + 4 (l / 16) + i; as the second operand of
 // O^T += V^T P^T they stay in place when the contraction runs over the keys in
 // that same order, which the transposing LDS read gives V.
+template <int D> struct StreamLds {
+    static constexpr int kJoin = 4 * 16 * (D + 4), kStage = 4 * 32 * D / 2;
+    __align__(16) float join[kJoin > kStage ? kJoin : kStage];   // first the waves' V stages
+    float join_ml[4 * 16 * 2];
+    AttnItem item;
+};
 template <int D, int RT, bool NT>
-__global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, AttnSplit s) {
+__device__ __forceinline__ void stream_bf16(const AttnArgs& a, const AttnSplit& s, int block,
+                                            StreamLds<D>& lds) {
     constexpr int KS = D < 32 ? 1 : D / 32;          // steps of 32 over the head
     constexpr int NB = D / 16;                       // value columns in 16s
     constexpr int VL = D / 16;                       // 16-byte loads per lane for 32 rows of V
     constexpr int CH = D / 8;                        // 16-byte pieces of a row
-    __shared__ __align__(16) float join[4 * 16 * (D + 4) > 4 * 32 * D / 2 ? 4 * 16 * (D + 4)
-                                                                         : 4 * 32 * D / 2];
-    __shared__ float join_ml[4 * 16 * 2];
-    __shared__ AttnItem shared_item;
-    const AttnItem it = attn_item(a, s, (int)blockIdx.x, shared_item);
+    const AttnItem it = attn_item(a, s, block, lds.item);
     if (!it.found) return;
     const int G = a.Hq / a.Hkv, wave = wave_id(), lane = threadIdx.x & 63;
     const int c16 = lane & 15, g4 = lane >> 4;
     const Keys keys = part_keys(a, s, it, G);
     const_int* table = table_row(a, it.req);
     const float scale = a.scale * kLog2e;
-    bf16* stage = (bf16*)join + wave * (32 * D);     // V of this wave's 32 keys
+    bf16* stage = (bf16*)lds.join + wave * (32 * D);     // V of this wave's 32 keys
 
     bf16x8 qf[RT][KS];
     int limit[RT];                                   // last visible position of the lane's row
@@ -380,14 +383,19 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, 
         const float sum = sum_quarters(l[rt]);
         __syncthreads();                             // stage and the last group's rows are free
         if (g4 == 0) {
-            join_ml[(wave * 16 + c16) * 2] = m[rt];
-            join_ml[(wave * 16 + c16) * 2 + 1] = sum;
+            lds.join_ml[(wave * 16 + c16) * 2] = m[rt];
+            lds.join_ml[(wave * 16 + c16) * 2 + 1] = sum;
         }
         for (int b = 0; b < NB; ++b)
-            *(f32x4*)(join + (wave * 16 + c16) * (D + 4) + 16 * b + 4 * g4) = acc[rt][b];
+            *(f32x4*)(lds.join + (wave * 16 + c16) * (D + 4) + 16 * b + 4 * g4) = acc[rt][b];
         __syncthreads();
-        join_waves<bf16, D>(a, s, it, G, rt * 16, join_ml, join);
+        join_waves<bf16, D>(a, s, it, G, rt * 16, lds.join_ml, lds.join);
     }
+}
+template <int D, int RT, bool NT>
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, AttnSplit s) {
+    __shared__ StreamLds<D> lds;
+    stream_bf16<D, RT, NT>(a, s, (int)blockIdx.x, lds);
 }
 
 // fp32, 16 keys a step. The contraction over the head takes element
@@ -588,14 +596,20 @@ __device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, const voi
 // which 16 bytes of the row each lane fetches is permuted (k_piece, v_piece4):
 // with 8 lanes' worth of banks in mind instead of 16, half of the LDS cycles
 // were conflicts.
+template <int D> struct TileLds {
+    __align__(128) bf16 k[2 * 64 * D], v[2 * 64 * D];
+    int gap_wave[4][4], odd_wave[4];
+    AttnItem item;
+};
 template <int D>
-__global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_tile_bf16(AttnArgs a, AttnSplit s) {
+__device__ __forceinline__ void tile_bf16(const AttnArgs& a, const AttnSplit& s, int block,
+                                          TileLds<D>& lds) {
     constexpr int KS = D / 16, NB = D / 32, CH = D / 8, LD = 16 * CH / 64;
     constexpr int kTile = 64 * D;                    // of K or V
-    __shared__ __align__(128) bf16 kbuf[2 * kTile], vbuf[2 * kTile];
-    __shared__ int gap_wave[4][4], odd_wave[4];
-    __shared__ AttnItem shared_item;
-    const AttnItem it = attn_item(a, s, (int)blockIdx.x, shared_item);
+    bf16 *const kbuf = lds.k, *const vbuf = lds.v;
+    int (&gap_wave)[4][4] = lds.gap_wave;
+    int (&odd_wave)[4] = lds.odd_wave;
+    const AttnItem it = attn_item(a, s, block, lds.item);
     if (!it.found) return;
     const int G = a.Hq / a.Hkv, wave = wave_id(), lane = threadIdx.x & 63;
     const int c32 = lane & 31, half = lane >> 5;
@@ -815,6 +829,28 @@ __global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_tile_bf16(
     if (a.lse && half == 0) a.lse[at.q] = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * kLn2;
 }
 
+template <int D>
+__global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_tile_bf16(AttnArgs a, AttnSplit s) {
+    __shared__ TileLds<D> lds;
+    tile_bf16<D>(a, s, (int)blockIdx.x, lds);
+}
+
+// Long and short requests of a call at once: the first n0 workgroups are the
+// tiles', the others the streams'. Two launches took the longer of the two
+// plus the other (25 + 13 us in a ragged batch).
+template <int D, bool NT>
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_both_bf16(AttnArgs a, AttnSplit s0,
+                                                                  AttnSplit s1, int n0) {
+    union Lds {
+        TileLds<D> tile;
+        StreamLds<D> stream;
+        __device__ Lds() {}
+    };
+    __shared__ Lds lds;
+    if ((int)blockIdx.x < n0) tile_bf16<D>(a, s0, (int)blockIdx.x, lds.tile);
+    else stream_bf16<D, 2, NT>(a, s1, (int)blockIdx.x - n0, lds.stream);
+}
+
 // Joins the parts of tiles that were cut, rows shared evenly by the workgroups.
 // A group of D / 4 lanes holds four columns each of a row. Few parts: every
 // group has a row of its own. Many: the groups share one row, each takes its
@@ -868,23 +904,13 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit 
         // (only where offsets decrease)
         if (!it.found || slot < 0 || slot + (long)step * (it.parts - 1) >= s.slots) continue;
         const int have = min(rows, it.n * G - (it.tile * s.R + row0));   // rows that exist
-        // parts p, p + by, ... of a row; eight at a time in flight
-        auto gather = [&](int row, int p, int by) {
+        auto part = [&](int row, int p) {
+            const bool in = p < it.parts;
+            const long from = (long)(slot + step * (in ? p : 0)) * s.R + row;
             Joined y;
-            for (; p < it.parts; p += 8 * by) {
-                Joined z[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const bool in = p + i * by < it.parts;
-                    const long at = (long)(slot + step * (in ? p + i * by : p)) * s.R + row;
-                    z[i].m = s.ml[at * 2];
-                    z[i].l = s.ml[at * 2 + 1];
-                    z[i].v = *(const f32x4*)(s.acc + at * D + d);
-                    if (!in) z[i].l = 0.f;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y.add(z[i]);
-            }
+            y.m = s.ml[from * 2];
+            y.l = in ? s.ml[from * 2 + 1] : 0.f;
+            y.v = *(const f32x4*)(s.acc + from * D + d);
             return y;
         };
         auto write = [&](const Joined& y, int row) {
@@ -895,11 +921,37 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit 
             if (a.lse && d == 0) a.lse[to.q] = y.l == 0.f ? -INFINITY : (y.m + __log2f(y.l)) * kLn2;
         };
         if (it.parts <= 8) {
-            for (int row = group; row < have; row += kGroups) write(gather(row0 + row, 0, 1), row0 + row);
+            // two rows, or two halves of the parts, in flight
+            for (int row = group; row < have; row += kGroups) {
+                Joined y[8], z;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) y[p] = part(row0 + row, p);
+                const int more = it.parts > 4 ? row : min(row + kGroups, have - 1);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) y[4 + p] = part(row0 + more, it.parts > 4 ? p + 4 : p);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) z.add(y[p]);
+                if (it.parts <= 4) {
+                    write(z, row0 + row);
+                    z = Joined();
+                    row += kGroups;
+                    if (row >= have) break;
+                }
+#pragma unroll
+                for (int p = 4; p < 8; ++p) z.add(y[p]);
+                write(z, row0 + row);
+            }
             continue;
         }
         for (int row = 0; row < have; ++row) {
-            const Joined y = gather(row0 + row, group, kGroups);
+            Joined y;
+            for (int p = group; p < it.parts; p += 8 * kGroups) {
+                Joined z[8];                         // eight parts in flight
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[i] = part(row0 + row, p + i * kGroups);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y.add(z[i]);
+            }
             __syncthreads();                         // the last row's shares are read
             *(f32x4*)&lds_v[group][d] = y.v;
             if (d == 0) { lds_ml[group][0] = y.m; lds_ml[group][1] = y.l; }
@@ -1008,25 +1060,23 @@ void launch_stream(const AttnArgs& a, const Plan& p, const Launch& l, hipStream_
         else attn_stream_f32<D, 2><<<grid, kAttnThreads, 0, st>>>(a, l.split);
     }
 }
-template <int D>
-void launch_tile(const AttnArgs& a, const Launch& l, hipStream_t st) {
-    attn_tile_bf16<D><<<(unsigned)l.items, kAttnThreads, 0, st>>>(a, l.split);
-}
 
 template <int D>
 hipError_t launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
-    for (int i = 0; i < p.n; ++i) {
-        const Launch& l = p.l[i];
-        if (i == 0 && p.tiles) {
-            if constexpr (D >= 64) launch_tile<D>(a, l, st);
-        } else {
-            launch_stream<D>(a, p, l, st);
+    const Launch &l0 = p.l[0], &l1 = p.l[p.n - 1];
+    if constexpr (D >= 64) {
+        const unsigned n0 = (unsigned)l0.items, n = n0 + (unsigned)l1.items;
+        if (p.n == 2) {
+            if (past_cache(a)) attn_both_bf16<D, true><<<n, kAttnThreads, 0, st>>>(a, l0.split, l1.split, (int)n0);
+            else attn_both_bf16<D, false><<<n, kAttnThreads, 0, st>>>(a, l0.split, l1.split, (int)n0);
+        } else if (p.tiles) {
+            attn_tile_bf16<D><<<n0, kAttnThreads, 0, st>>>(a, l0.split);
         }
     }
-    const AttnSplit &s0 = p.l[0].split, &s1 = p.l[p.n - 1].split;
-    const int n0 = (int)p.l[0].joins, n = n0 + (p.n > 1 ? (int)p.l[1].joins : 0);
-    if (a.bf16_io) attn_join<bf16, D><<<(unsigned)n, kAttnThreads, 0, st>>>(a, s0, s1, n0);
-    else attn_join<float, D><<<(unsigned)n, kAttnThreads, 0, st>>>(a, s0, s1, n0);
+    if (!p.tiles) launch_stream<D>(a, p, l0, st);
+    const int n0 = (int)l0.joins, n = n0 + (p.n > 1 ? (int)l1.joins : 0);
+    if (a.bf16_io) attn_join<bf16, D><<<(unsigned)n, kAttnThreads, 0, st>>>(a, l0.split, l1.split, n0);
+    else attn_join<float, D><<<(unsigned)n, kAttnThreads, 0, st>>>(a, l0.split, l1.split, n0);
     return hipGetLastError();
 }
 

@@ -101,32 +101,67 @@ __device__ __forceinline__ int find(const int* off, int n, int x) {
     }
     return lo;
 }
+// The same for 64 neighbouring x of a wave (x of lane 0 is the least, and
+// inside): the wave narrows the range of the first by 64 a step, and the
+// others look among the 63 offsets that follow; only x of more requests than
+// that search by themselves. Two or three memory latencies instead of ten.
+__device__ __forceinline__ int find_wave(const int* off, int n, int x, bool in) {
+    const int lane = threadIdx.x & 63;
+    const int x0 = __builtin_amdgcn_readfirstlane(x);
+    int lo = 0, hi = n;                  // off[lo] <= x0 < off[hi]
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 63) >> 6;
+        const int at = lo + lane * step;
+        const unsigned long long le = __ballot(at < hi && off[at < hi ? at : lo] <= x0);
+        // lanes that hold: 0 .. k
+        const int k = 63 - __builtin_clzll(le);
+        const int next = lo + (k + 1) * step;
+        lo += k * step;
+        hi = next < hi ? next : hi;
+    }
+    const int at = lo + 1 + lane;
+    const int border = at < n ? off[at] : INT32_MAX;   // of the requests behind
+    int i = 0;
+    for (int bit = 32; bit; bit >>= 1)                 // borders <= x among them
+        if (__shfl(border, i + bit - 1) <= x) i += bit;
+    if (in && i == 63 && lo + 64 < n && off[lo + 64] <= x) return find(off, n, x);
+    return lo + i;
+}
 
+// Entry x of the ring from head, x <= pool.
+__device__ __forceinline__ int ring_at(const PlanArgs& a, int head, int x) {
+    const unsigned i = (unsigned)head + (unsigned)x;
+    return (int)(i >= (unsigned)a.pool ? i - (unsigned)a.pool : i);
+}
+
+// `first` counts threads: whole waves are consecutive and aligned.
 __device__ void fill(const PlanArgs& a, const PlanWs& w, long first, long step) {
     const int B = a.B, mask = (1 << a.page_shift) - 1;
     const int head = w.ring[0], count = w.ring[1];
     const int tokens = a.cu[B], taken = w.taken[B], given = w.given[B];
-    const long all = (long)a.n_slots + taken + given;
+    // the slots fill whole waves, so that the lanes of a wave search together
+    const long slots = ((long)a.n_slots + 63) & ~63l;
+    const long all = slots + taken + given;
     for (long j = first; j < all; j += step) {
-        if (j < a.n_slots) {
+        if (j < slots) {
             const int t = (int)j;
-            int slot = -1;
+            int slot = -1, i = 0;
+            // the wave's first slot has a token if any of them has
+            if (__builtin_amdgcn_readfirstlane(t) < tokens) i = find_wave(a.cu, B, t, t < tokens);
             if (t < tokens) {
-                const int i = find(a.cu, B, t);
                 const int pos = a.kept[i] + (t - a.cu[i]), pg = pos >> a.page_shift;
                 const int page = pg < w.have[i]
                     ? a.table[(long)i * a.width + pg]
-                    : a.ring[((long)head + w.taken[i] + pg - w.have[i]) % a.pool];
+                    : a.ring[ring_at(a, head, w.taken[i] + pg - w.have[i])];
                 slot = (page << a.page_shift) + (pos & mask);
             }
-            a.slots[t] = slot;
-        } else if (j < (long)a.n_slots + taken) {
-            const int x = (int)(j - a.n_slots), i = find(w.taken, B, x);
-            a.table[(long)i * a.width + w.have[i] + (x - w.taken[i])] =
-                a.ring[((long)head + x) % a.pool];
+            if (t < a.n_slots) a.slots[t] = slot;
+        } else if (j < slots + taken) {
+            const int x = (int)(j - slots), i = find(w.taken, B, x);
+            a.table[(long)i * a.width + w.have[i] + (x - w.taken[i])] = a.ring[ring_at(a, head, x)];
         } else {
-            const int x = (int)(j - a.n_slots - taken), i = find(w.given, B, x);
-            a.ring[((long)head + count + x) % a.pool] =
+            const int x = (int)(j - slots - taken), i = find(w.given, B, x);
+            a.ring[ring_at(a, head, count + x)] =
                 a.table[(long)i * a.width + a.pages_out[i] + (x - w.given[i])];
         }
     }
@@ -185,7 +220,7 @@ __global__ __launch_bounds__(kThreads) void page_plan_scan(PlanArgs a, void* ws,
         w.ring[0] = head;
         w.ring[1] = count;
         a.cu[a.B] = ok ? (int)all.tokens : 0;
-        a.ring_out[0] = taken ? (int)(((long)head + taken) % a.pool) : head;
+        a.ring_out[0] = taken ? ring_at(a, head, taken) : head;
         a.ring_out[1] = count - taken + given;
         a.status[0] = status;
     }

@@ -147,10 +147,11 @@ __device__ __forceinline__ const_int* table_row(const AttnArgs& a, int req) {
     return (const_int*)(uintptr_t)(a.table + (long)req * a.width);
 }
 // Page id of the 16 positions at pos (a multiple of 16), -1 when there is none.
+// Behind the end (end > 0) the last page's entry is read instead: no branch,
+// so that several loads are in flight at once.
 __device__ __forceinline__ int page_at(const AttnArgs& a, const_int* table, int pos, int end) {
-    if (pos >= end) return -1;
-    const int p = table[pos >> a.page_shift];
-    return (unsigned)p < (unsigned)a.pool ? p : -1;
+    const int p = table[min(pos, end - 1) >> a.page_shift];
+    return pos < end && (unsigned)p < (unsigned)a.pool ? p : -1;
 }
 
 // Which 16-byte piece of a row of D values LDS holds in place of piece c, so
@@ -223,7 +224,8 @@ __device__ __forceinline__ void stream_bf16(const AttnArgs& a, const AttnSplit& 
     }
 
     bf16x8 kf[2][KS], vf[VL];
-    int page[2], page_next[2];
+    // pages of the 32 keys at hand and, a step ahead of their loads, of the next
+    int page[2] = {-1, -1}, page_next[2] = {-1, -1};
     const int row_mask = (1 << a.page_shift) - 1;
     auto base_of = [&](int p, int pos) {             // row of the plane of head h
         return (((long)p * a.Hkv + it.h) << a.page_shift) + (pos & row_mask);
@@ -264,16 +266,18 @@ __device__ __forceinline__ void stream_bf16(const AttnArgs& a, const AttnSplit& 
         for (int u = 0; u < 2; ++u) kf[u][0] = bf16x8{};
 
     int pos = keys.begin + wave * 32;
-    page[0] = page_at(a, table, pos, keys.end);
-    page[1] = page_at(a, table, pos + 16, keys.end);
     if (pos < keys.end) {
+        page[0] = page_at(a, table, pos, keys.end);
+        page[1] = page_at(a, table, pos + 16, keys.end);
+        page_next[0] = page_at(a, table, pos + 128, keys.end);
+        page_next[1] = page_at(a, table, pos + 144, keys.end);
         load_k(pos);
         load_v(pos);
     }
     for (; pos < keys.end; pos += 128) {
         const int next = pos + 128;
-        page_next[0] = page_at(a, table, next, keys.end);
-        page_next[1] = page_at(a, table, next + 16, keys.end);
+        const int page_2 = page_at(a, table, next + 128, keys.end);
+        const int page_3 = page_at(a, table, next + 144, keys.end);
         const bool gap0 = page[0] < 0, gap1 = page[1] < 0;
         f32x4 st[RT][2];
         for (int rt = 0; rt < RT; ++rt)
@@ -307,6 +311,8 @@ __device__ __forceinline__ void stream_bf16(const AttnArgs& a, const AttnSplit& 
             load_k(next);
             load_v(next);
         }
+        page_next[0] = page_2;
+        page_next[1] = page_3;
         bf16x8 pf[RT];
         float pe[RT][2][4];
         for (int rt = 0; rt < RT; ++rt) {
@@ -467,14 +473,16 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_f32(AttnArgs a, A
     };
 
     int pos = keys.begin + wave * 16;
-    int page = page_at(a, table, pos, keys.end);
+    int page = -1, page_next = -1;
     if (pos < keys.end) {
+        page = page_at(a, table, pos, keys.end);
+        page_next = page_at(a, table, pos + 64, keys.end);
         load_k(page, pos);
         load_v(page, pos);
     }
     for (; pos < keys.end; pos += 64) {
         const int next = pos + 64;
-        const int page_next = page_at(a, table, next, keys.end);
+        const int page_2 = page_at(a, table, next + 64, keys.end);
         f32x4 st[RT];
         for (int rt = 0; rt < RT; ++rt) {
             f32x4 x = zero4();
@@ -544,6 +552,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_f32(AttnArgs a, A
                 for (int rt = 0; rt < RT; ++rt) acc[rt][b] = mma4(vf[i][b], pe[rt][i], acc[rt][b]);
         if (next < keys.end) load_v(page_next, next);
         page = page_next;
+        page_next = page_2;
     }
 
     for (int rt = 0; rt < RT; ++rt) {
@@ -889,8 +898,9 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit 
         if (threadIdx.x == 0) shared_units = sched.items;
     }
     __syncthreads();
-    // an even share of the rows of all cut tiles, at most 2^11 tiles * 2^8
-    const unsigned all = (unsigned)uniform(shared_units) << s.R_log2;
+    // an even share of the rows of all cut tiles (more of them than partial
+    // results there are only where offsets decrease)
+    const unsigned all = (unsigned)min(max(uniform(shared_units), 0), s.slots) << s.R_log2;
     const unsigned share = (all + blocks - 1) / blocks;
     const unsigned row_end = min(all, share * (block + 1));
     for (unsigned r = share * block; r < row_end;) {
@@ -1005,7 +1015,7 @@ Launch launch_of(long T, long B, long G, long Hkv, int R, int unit, int most_log
     const long target = 1l << most_log2;
     const long tiles = max_rows <= R ? (B < T ? B : T) * Hkv : attn_max_tiles(T, B, G, Hkv, R);
     l.items = attn_max_items(tiles, target);
-    l.split.slots = (int)attn_max_slots(target);
+    l.split.slots = (int)attn_max_slots(tiles, target);
     // the joining's: a row or more each (2048 workgroups: 7 to 9 us more where
     // there is little to join, no less where there is much)
     const long rows = (tiles < target ? tiles : target) * R;

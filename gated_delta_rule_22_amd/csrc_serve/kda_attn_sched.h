@@ -61,7 +61,7 @@ __device__ __forceinline__ AttnReq attn_req(const AttnArgs& a, const AttnSplit& 
     r.row0 = lo;
     r.n = in ? max(hi - lo, 0) : 0;
     r.kept = min(max(kept, 0), cap);
-    r.kv = min(r.kept + r.n, cap);
+    r.kv = r.kept + min(r.n, cap - r.kept);
     const int rows = r.n * (a.Hq / a.Hkv);           // at most T Hq
     r.tiles = rows >= s.min_rows && rows <= s.max_rows ? (rows + s.R - 1) >> s.R_log2 : 0;
     return r;
@@ -254,7 +254,10 @@ __device__ __forceinline__ AttnItem attn_item(const AttnArgs& a, const AttnSplit
 // Bounds of the host: parts of a call whose tiles number at most `tiles`
 // (KV heads included), and partial results.
 inline long attn_max_items(long tiles, long target) { return tiles + target + 16; }
-inline long attn_max_slots(long target) { return 2 * target + 16; }
+// (a tile that is cut has two parts or more, and fewer than twice its keys / C)
+inline long attn_max_slots(long tiles, long target) {
+    return (tiles < target ? tiles : target) + target + 16;
+}
 inline long attn_max_tiles(long T, long B, long G, long Hkv, long R) {
     return (T * G / R + (B < T ? B : T)) * Hkv;
 }

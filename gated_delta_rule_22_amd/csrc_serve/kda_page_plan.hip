@@ -83,7 +83,8 @@ __device__ __forceinline__ Request request(const PlanArgs& a, int i) {
     if (i >= a.B) return r;
     const long kept = a.kept[i], fresh = a.fresh[i], have = a.pages_in[i];
     const long need = (kept + fresh + (1l << a.page_shift) - 1) >> a.page_shift;
-    r.c.bad = kept < 0 || fresh < 0 || have < 0 || have > a.width || need > a.width;
+    r.c.bad = kept < 0 || fresh < 0 || have < 0 || have > a.width || need > a.width ||
+              kept + fresh > INT32_MAX;
     r.have = (int)have;
     r.need = (int)need;
     r.c.tokens = fresh;
@@ -153,7 +154,8 @@ __device__ void fill(const PlanArgs& a, const PlanWs& w, long first, long step) 
                 const int page = pg < w.have[i]
                     ? a.table[(long)i * a.width + pg]
                     : a.ring[ring_at(a, head, w.taken[i] + pg - w.have[i])];
-                slot = (page << a.page_shift) + (pos & mask);
+                // (a page id that is none gives no slot rather than another page's)
+                if ((unsigned)page < (unsigned)a.pool) slot = (page << a.page_shift) + (pos & mask);
             }
             if (t < a.n_slots) a.slots[t] = slot;
         } else if (j < slots + taken) {

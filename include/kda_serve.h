@@ -44,7 +44,8 @@ extern "C" {
  * Block tables and slot maps from request lengths.
  *
  * Request i keeps kept_len[i] tokens in the cache and adds n_new[i] (both
- * >= 0; both 0 for a request that has ended or an unused row). It needs
+ * >= 0, at most INT32_MAX together; both 0 for a request that has ended or an
+ * unused row). It needs
  * ceil((kept + new) / page_size) pages and holds n_pages_in[i] of them,
  * block_table[i, 0 .. n_pages_in[i]). Missing pages are taken from the pool
  * in the order of requests and positions, surplus ones go back in that order.
@@ -59,7 +60,8 @@ extern "C" {
  *   cu_new      [B + 1]  exclusive prefix sum of n_new: request i's new tokens
  *               are rows cu_new[i] .. cu_new[i + 1) of the step's packed tensors
  *   slot_map    [n_slots]  slot (page * page_size + offset) of every new token;
- *               -1 in the rows behind cu_new[B] (a padded step)
+ *               -1 in the rows behind cu_new[B] (a padded step), and where the
+ *               page id is outside [0, n_pool)
  *   status      [1]  see above. When it is not KDA_PLAN_OK the step is empty:
  *               nothing is taken or given back (n_pages_out = n_pages_in,
  *               ring_out = ring_in), cu_new is 0 throughout and slot_map -1.

@@ -131,6 +131,68 @@ def test_masked_values_stay_out(n, ctx, what, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,ctx", [(1, 500), (8, 300), (70, 90)])
+def test_seen_nan_keys_give_nan(n, ctx, dtype):
+    # keys that every row sees: the rows of their heads are NaN, others are not
+    c = R.attn_case([n, 2], [ctx, 20], 8, 2, 64, 16, dtype, seed=63)
+    ref = R.attn(c)
+    for pos in range(0, 90, 3):                     # all of some waves' keys, too
+        c["kc"][c["table"][0, pos // 16], 0, pos % 16] = float("nan")
+    o, lse = call(c)
+    assert torch.isnan(o[:n, :4]).all() and torch.isnan(lse[:n, :4]).all()
+    o[:n, :4], lse[:n, :4] = ref[0][:n, :4].to(o.dtype), ref[1][:n, :4].float()
+    verdict(c, o, lse, ref)
+    c["kc"][c["table"][0, :6].long()] = float("nan")
+    o, lse = call(c)
+    assert torch.isnan(o[:n]).all() and torch.isnan(lse[:n]).all()
+
+
+@pytest.mark.parametrize("n", [1, 70])
+def test_two_graphs_with_their_own_workspaces(n):
+    # captured on two lengths, replayed in turn, each with the tensors it made
+    cases = [R.attn_case([n, 1], ctx, 8, 2, 64, 16, BF, seed=64 + i)
+             for i, ctx in enumerate([[2500, 40], [300, 4000]])]
+    refs, graphs, outs, keep = [], [], [], []
+    for c in cases:
+        dev = [c[k].to(DEV) for k in ("q", "kc", "vc", "table")] + [ints(c["kept"]), ints(c["cu"])]
+        keep.append(dev)
+        refs.append(R.attn(c))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            kda.kda_attn_paged(*dev, max_new=n)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(kda.kda_attn_paged(*dev, max_new=n, want_lse=True))
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1):
+        graphs[i].replay()
+        graphs[1 - i].replay()
+        torch.cuda.synchronize()
+        for c, ref, (o, lse) in zip(cases, refs, outs):
+            verdict(c, o.cpu(), lse.cpu(), ref)
+        kda.kda_attn_paged(*keep[i], max_new=n)     # eager calls in between
+
+
+def test_overlapping_offsets_end():
+    # every request claims all rows: values are unspecified, the call ends and
+    # writes nothing behind its rows
+    B, T = 64, 300
+    c = R.attn_case([T], [700], 8, 2, 64, 16, BF, seed=66, spare_rows=3)
+    dev = {k: c[k].to(DEV) for k in ("q", "kc", "vc")}
+    table = c["table"].to(DEV).expand(B, -1).contiguous()
+    cu = ints([0, T] * (B // 2) + [0])
+    for hint in (0, 1):
+        o = torch.full(c["q"].shape, 7.0, dtype=BF, device=DEV)
+        kda.kda_attn_paged(dev["q"], dev["kc"], dev["vc"], table, ints([700] * B), cu, o=o,
+                           max_new=hint)
+        torch.cuda.synchronize()
+        assert bool((o[T:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("n", [1, 8, 70])
 def test_pages_outside_the_pool_are_masked(n, dtype):
     c = R.attn_case([n, n, n], [200, 90, 0], 8, 2, 64, 16, dtype, seed=54)

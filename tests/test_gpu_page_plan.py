@@ -178,3 +178,20 @@ def test_refuses_wrong_arguments():
             kda.kda_page_plan(*b, page_size=16, n_slots=4)
     with pytest.raises(kda.KDAError):       # an output over an input
         kda.kda_page_plan(*a, page_size=16, slot_map=a[1])
+
+
+def test_page_ids_outside_the_pool_give_no_slot():
+    c = dict(kept=[60, 0], new=[10, 3], pages=[2, 0], table=[[0, 2**26, 0], [0, 0, 0]],
+             ring=[5, -3, 2**31 - 1, 1, 0, 2], ring_state=[0, 3], page=64, slots=25)
+    got = call(c)
+    assert got["status"] == 0
+    # page 0 of request 0 is valid, its second is no page; request 1 takes page 5
+    assert got["slot"][:4] == [60, 61, 62, 63] and set(got["slot"][4:10]) == {-1}
+    assert got["slot"][10:13] == [320, 321, 322]
+
+
+def test_many_pages_move_in_a_small_step():
+    # few slots, thousands of pages given back and taken
+    c = make(31, 300, 16, 2, 6000, gone=0.5)
+    c["slots"] = max(c["slots"], sum(c["new"]))
+    assert check(c, in_place=True)["status"] == 0

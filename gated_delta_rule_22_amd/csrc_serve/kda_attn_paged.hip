@@ -848,7 +848,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_tile_bf16(
 // tiles', the others the streams'. Two launches took the longer of the two
 // plus the other (25 + 13 us in a ragged batch).
 template <int D, bool NT>
-__global__ __launch_bounds__(kAttnThreads, 2) void attn_both_bf16(AttnArgs a, AttnSplit s0,
+__global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_both_bf16(AttnArgs a, AttnSplit s0,
                                                                   AttnSplit s1, int n0) {
     union Lds {
         TileLds<D> tile;

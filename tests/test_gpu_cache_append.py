@@ -58,6 +58,24 @@ def test_cache_past_32_bit_offsets():
     assert bool((kc[pool - 1, :, 1:page - 1] == 4.0).all())
 
 
+@pytest.mark.parametrize("dtype,H", [(torch.float32, 5), (torch.bfloat16, 9)])
+def test_large_calls(dtype, H):
+    # more than the last-level cache holds: other loads and stores
+    T, d, page = 70001, 128, 32
+    pool = -(-T // page) + 1
+    g = torch.Generator(device=DEV).manual_seed(3)
+    k, v = (torch.randn((T, H, d), generator=g, device=DEV).to(dtype) for _ in range(2))
+    slot = torch.randperm(pool * page, generator=g, device=DEV)[:T].to(torch.int32)
+    slot[::1000] = -1
+    kc, vc = (torch.full((pool, H, page, d), -2.0, dtype=dtype, device=DEV) for _ in range(2))
+    kda.kda_cache_append(k, v, slot, kc, vc)
+    keep = slot >= 0
+    s = slot[keep].long()
+    for cache, rows in ((kc, k), (vc, v)):
+        assert torch.equal(cache[s // page, :, s % page], rows[keep])
+        assert int((cache == -2.0).all(-1).sum()) >= (pool * page - int(keep.sum())) * H
+
+
 def test_empty_and_refusals():
     kc = torch.zeros((2, 2, 16, 64), device=DEV)
     vc = torch.zeros_like(kc)

@@ -861,9 +861,9 @@ __global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_both_bf16(
 }
 
 // Joins the parts of tiles that were cut, rows shared evenly by the workgroups.
-// A group of D / 4 lanes holds four columns each of a row. Few parts: every
-// group has a row of its own. Many: the groups share one row, each takes its
-// share of the parts, and the shares join through LDS. A part without a key
+// A group of D / 4 lanes holds four columns each of a row. Up to 16 parts every
+// group has a row of its own. With more the groups share one row, each takes
+// its share of the parts, and the shares join through LDS. A part without a key
 // of the row has l = 0 (and NaN scores leave m at -infinity, but not l at 0).
 struct Joined {
     float m = -INFINITY, l = 0.f;
@@ -930,26 +930,36 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit 
             for (int i = 0; i < 4; ++i) o[i] = from_f32<T>(y.v[i] * inv);
             if (a.lse && d == 0) a.lse[to.q] = y.l == 0.f ? -INFINITY : (y.m + __log2f(y.l)) * kLn2;
         };
-        if (it.parts <= 8) {
-            // two rows, or two halves of the parts, in flight
-            for (int row = group; row < have; row += kGroups) {
-                Joined y[8], z;
+        if (it.parts <= 4) {                         // two rows in flight
+            for (int row = group; row < have; row += 2 * kGroups) {
+                const int other = min(row + kGroups, have - 1);
+                Joined y[8], z, z1;
 #pragma unroll
-                for (int p = 0; p < 4; ++p) y[p] = part(row0 + row, p);
-                const int more = it.parts > 4 ? row : min(row + kGroups, have - 1);
-#pragma unroll
-                for (int p = 0; p < 4; ++p) y[4 + p] = part(row0 + more, it.parts > 4 ? p + 4 : p);
-#pragma unroll
-                for (int p = 0; p < 4; ++p) z.add(y[p]);
-                if (it.parts <= 4) {
-                    write(z, row0 + row);
-                    z = Joined();
-                    row += kGroups;
-                    if (row >= have) break;
+                for (int p = 0; p < 4; ++p) {
+                    y[p] = part(row0 + row, p);
+                    y[4 + p] = part(row0 + other, p);
                 }
 #pragma unroll
-                for (int p = 4; p < 8; ++p) z.add(y[p]);
+                for (int p = 0; p < 4; ++p) {
+                    z.add(y[p]);
+                    z1.add(y[4 + p]);
+                }
                 write(z, row0 + row);
+                if (row + kGroups < have) write(z1, row0 + other);
+            }
+            continue;
+        }
+        if (it.parts <= 16) {                        // eight parts in flight
+            for (int row = group; row < have; row += kGroups) {
+                Joined y;
+                for (int p = 0; p < it.parts; p += 8) {
+                    Joined z[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) z[i] = part(row0 + row, p + i);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y.add(z[i]);
+                }
+                write(y, row0 + row);
             }
             continue;
         }
@@ -1028,7 +1038,7 @@ Plan plan_of(int T, int B, int Hq, int Hkv, int d, int max_new, bool bf16_io) {
     p.tiles = bf16_io && d >= 64 && most > kStreamRows;
     p.RT = most <= 16 ? 1 : 2;
     if (p.tiles) {
-        p.l[p.n] = launch_of(T, B, G, Hkv, kTileRows, 64, 9, 9, 9, INT32_MAX);
+        p.l[p.n] = launch_of(T, B, G, Hkv, kTileRows, 128, 9, 9, 9, INT32_MAX);
         p.l[p.n].split.min_rows = kStreamRows + 1;
         ++p.n;
     }

@@ -111,7 +111,8 @@ __device__ __forceinline__ void join_waves(const AttnArgs& a, const AttnSplit& s
         const long slot = (long)it.slot + ((long)it.part * it.tiles + it.tile) * a.Hkv + it.h;
         if ((unsigned long)slot >= (unsigned long)s.slots) return;   // only where offsets decrease
         const long at = slot * s.R + r0 + row;
-        for (int i = 0; i < kPer; i += 4)
+        // (a row without a key in this part has l = 0, and its values are not read)
+        for (int i = 0; l != 0.f && i < kPer; i += 4)
             *(f32x4*)(s.acc + at * D + d + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
         if (d == 0) { s.ml[at * 2] = m; s.ml[at * 2 + 1] = l; }
         return;
@@ -816,7 +817,8 @@ __device__ __forceinline__ void tile_bf16(const AttnArgs& a, const AttnSplit& s,
         const long slot = (long)it.slot + ((long)it.part * it.tiles + it.tile) * a.Hkv + it.h;
         if ((unsigned long)slot >= (unsigned long)s.slots) return;   // only where offsets decrease
         float* x = s.acc + (slot * s.R + row) * D;
-        for (int b = 0; b < NB; ++b)
+        // (a row without a key in this part has l = 0, and its values are not read)
+        for (int b = 0; sum != 0.f && b < NB; ++b)
             for (int i = 0; i < 16; i += 4)
                 *(f32x4*)(x + 32 * b + 2 * i + 4 * half) =
                     f32x4{acc[b][i], acc[b][i + 1], acc[b][i + 2], acc[b][i + 3]};

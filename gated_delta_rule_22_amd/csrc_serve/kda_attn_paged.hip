@@ -12,7 +12,12 @@
 // rows and a part of its keys (kda_attn_sched.h); its four waves take 32
 // (fp32: 16) keys each in turn and run free of each other, so that every wave
 // has its next keys and values in flight while it computes. Their rows are
-// joined through LDS at the end.
+// joined through LDS at the end. bf16, 32 query heads over 8 of 128: one token
+// of 256 requests over 1024 to 16384 positions (5.8 GB) 965 + 7 us, 6.0 TB/s;
+// 8 tokens of 4 over 65536 to 262144 (2.6 GB) 425 + 8 us, 6.2 TB/s; one token
+// over 1000 positions 7.5 + 4.3 us, all of it latency. fp32, 16 heads over 4:
+// 64 tokens over 4096 positions (1.1 GB) 200 us, 5.4 TB/s; 1024 tokens over
+// 1024 of width 64 83 us, half of the fp32 matrix rate.
 #include "kda_attn_sched.h"
 
 namespace kda {
@@ -602,6 +607,13 @@ __device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, const voi
 // while the exponentials of these run, so that the matrix cores have work in
 // both; K is therefore fetched two steps ahead and V one, two buffers each.
 //
+// 8192 tokens over 24576 positions, 32 heads over 8 of 128: 3.6 to 3.95 ms
+// from card to card, 0.98 to 1.06 PFLOP/s, with the matrix cores busy 46% of
+// the cycles at 2.0 GHz: the clock falls as they fill, and a library product
+// of 8192^3 reaches 1.20 PFLOP/s there. (Scores of the next 64 keys made while
+// the exponentials of these run, K fetched two steps ahead: the same at width
+// 128, 8% longer at 64, where the registers leave a workgroup less.)
+//
 // K and V go from memory to LDS directly, 16 bytes a lane in the lanes' order;
 // which 16 bytes of the row each lane fetches is permuted (k_piece, v_piece4):
 // with 8 lanes' worth of banks in mind instead of 16, half of the LDS cycles
@@ -997,8 +1009,14 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit 
 // max_new * G (T * G when the largest is not known).
 //
 // Up to kStreamRows rows a request is the stream kernels'; of a call with
-// larger ones (bf16, d of 64 and 128) those go to the tile kernel, and the
-// rest to a second launch.
+// larger ones (bf16, d of 64 and 128) those are the tile kernel's. At 64: 64
+// requests of 64 rows over 4000 positions 187 -> 291 us, 16 over 2000 42 -> 36
+// us. Parts: see AttnSplit. Streams, at most 2048 and at least 1024 of them
+// (4 long contexts: 480 us with 2048, 425 with 1024), 256 short ones (with 512:
+// 31 + 13 us in a ragged fp32 batch instead of 28 + 5). Tiles, 512, what the
+// card holds at once (256: 512 tokens over 3000 positions 53 instead of 44 us,
+// 1024: 52), of 128 keys or more (64: 528 tokens of 4 heads 16 instead of 13
+// us, 512: 17).
 constexpr int kStreamRows = 32;
 
 struct Launch {

@@ -20,9 +20,9 @@ namespace {
 
 constexpr int kAttnThreads = 256;
 // Starting a part costs about as much as 1024 of its keys: more parts than
-// there is room for on the card balance uneven lengths, but not below this
-// length (a batch of 480 short fp32 tiles: 29 us with 2048 parts, see the
-// kernels for the rest).
+// there is room for on the card balance uneven lengths, but are not made
+// shorter than this for it (a ragged fp32 batch of few keys: 45 us with up to
+// 2048 parts, 32 us with 256).
 constexpr int kLongPart = 1024;
 
 // What a launch works on, besides AttnArgs.
@@ -79,6 +79,25 @@ __device__ __forceinline__ int wave_prefix(int x) {
     return x;
 }
 
+// Sum over the wave.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ long dpp_add(long x) {
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(x >> 32), CTRL, ROWS, 0xF, false);
+    return x + (long)((unsigned long)(unsigned)lo | (unsigned long)(unsigned)hi << 32);
+}
+__device__ __forceinline__ long wave_total(long x) {
+    x = dpp_add<0x111, 0xF>(x);
+    x = dpp_add<0x112, 0xF>(x);
+    x = dpp_add<0x114, 0xF>(x);
+    x = dpp_add<0x118, 0xF>(x);
+    x = dpp_add<0x142, 0xA>(x);
+    x = dpp_add<0x143, 0xC>(x);
+    const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)x, 63);
+    const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)(x >> 32), 63);
+    return (long)((unsigned long)lo | (unsigned long)hi << 32);
+}
+
 // 256 requests of one wave, four a lane: what they were cut into. UNITS
 // counts the tiles that were cut (for joining them), otherwise the parts.
 template <bool UNITS>
@@ -101,9 +120,9 @@ struct AttnBlock {
         r3 = attn_req(a, s, i + 3 <= last, u3, u4, k3);
     }
     __device__ int tiles() const { return r0.tiles + r1.tiles + (r2.tiles + r3.tiles); }
-    __device__ float cost() const {
-        return (float)r0.tiles * (float)r0.kv + (float)r1.tiles * (float)r1.kv +
-               ((float)r2.tiles * (float)r2.kv + (float)r3.tiles * (float)r3.kv);
+    __device__ long cost() const {
+        return (long)r0.tiles * r0.kv + (long)r1.tiles * r1.kv +
+               ((long)r2.tiles * r2.kv + (long)r3.tiles * r3.kv);
     }
     // ceil(kv / C) in fp32: C is a multiple of 64, so the quotient is off by
     // less than 2^-24 * 2^24 / 64 and one comparison mends it
@@ -164,8 +183,9 @@ struct AttnBlock {
 };
 
 // The first wave's view of the call. Every workgroup of every kernel of a call
-// computes the same C: the sum of the work runs in fp32 in a fixed order, and
-// the bounds below leave room for its rounding.
+// computes the same C: the work is summed in whole numbers, and what follows
+// has no product that one compiled kernel could fuse with a sum and another
+// not. The bounds below leave room for its rounding.
 template <bool UNITS>
 struct AttnSched {
     AttnBlock<UNITS> first;
@@ -173,16 +193,17 @@ struct AttnSched {
 
     __device__ void init(const AttnArgs& a, const AttnSplit& s) {
         first.load(a, s, 0);
-        float cost = first.cost(), tiles = (float)first.tiles();
+        long cost = first.cost();
+        int tiles = first.tiles();
         for (int base = 256; base < a.B; base += 256) {
             AttnBlock<UNITS> b;
             b.load(a, s, base);
             cost += b.cost();
-            tiles += (float)b.tiles();
+            tiles += b.tiles();
         }
-        const float total = wave_sum_uniform(cost) * (float)a.Hkv;
-        tiles = wave_sum_uniform(tiles) * (float)a.Hkv;
-        const float parts = fminf(fmaxf(tiles, (float)(1 << s.some_log2)), (float)(1 << s.most_log2));
+        const float total = (float)(wave_total(cost) * a.Hkv);
+        const float all = (float)(__builtin_amdgcn_readlane(wave_prefix(tiles), 63) * a.Hkv);
+        const float parts = fminf(fmaxf(all, (float)(1 << s.some_log2)), (float)(1 << s.most_log2));
         const float most = total / parts;
         const float few = total * __builtin_bit_cast(float, (127 - s.few_log2) << 23);
         const float want = fmaxf(most, fminf(few, (float)kLongPart));

@@ -3,6 +3,8 @@
 Unused cache rows, table entries and query rows hold NaN or nonsense
 (serve_ref.attn_case), so every case also checks that they do not reach the
 result. Bounds: serve_ref.attn_bound, element by element."""
+import random
+
 import pytest
 import torch
 
@@ -346,3 +348,16 @@ def test_refusals():
     for s in (-1.0, float("nan")):
         with pytest.raises(kda.KDAError):
             kda.kda_attn_paged(q, kc, vc, tab, kept, cu, scale=s)
+
+
+@pytest.mark.parametrize("seed", range(10))
+def test_random_batches(seed):
+    # lengths from nothing to thousands of keys, cut into parts of any length
+    rng = random.Random(seed)
+    B = rng.choice([1, 2, 3, 7, 20])
+    n = [rng.choice([0, 1, 1, 2, 8, 31, rng.randint(1, 150)]) for _ in range(B)]
+    ctx = [int(2 ** rng.uniform(0, 12.5)) for _ in range(B)]
+    Hkv = rng.choice([1, 2, 3])
+    c = R.attn_case(n, ctx, Hkv * rng.choice([1, 3, 4]), Hkv, rng.choice([16, 32, 64, 128]),
+                    rng.choice([16, 64, 256]), rng.choice([BF, F32]), seed=seed, spare_rows=2)
+    check(c, max_new=rng.choice([0, 0, max(n)]))

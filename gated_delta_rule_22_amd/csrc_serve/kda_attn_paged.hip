@@ -351,8 +351,8 @@ __device__ __forceinline__ void stream_bf16(const AttnArgs& a, const AttnSplit& 
                     pe[rt][u][i] = p;
                 }
             l[rt] += sum;
-            // the weights are rounded to bf16 for the matrix cores (2^-9 on
-            // average); l sums them unrounded
+            // the weights are rounded to bf16 for the matrix cores (at most 2^-8 each,
+            // see the test bounds); l sums them unrounded
             pf[rt] = pack8(f32x4{pe[rt][0][0], pe[rt][0][1], pe[rt][0][2], pe[rt][0][3]},
                            f32x4{pe[rt][1][0], pe[rt][1][1], pe[rt][1][2], pe[rt][1][3]});
         }

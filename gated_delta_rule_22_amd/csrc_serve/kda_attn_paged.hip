@@ -592,7 +592,7 @@ __device__ __forceinline__ float max_halves(float x) { return fmaxf(x, __shfl_xo
 // transposing load; there is no result register, and the kernel waits itself.
 __device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, const void* base) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 ::"s"(to), "v"(off), "s"(base) : "memory");
+                 ::"s"(to), "v"(off), "s"(base) : "memory", "m0");
 }
 
 // Prompts: tiles of 128 rows, 32 per wave, against 64 keys at a time that all

@@ -56,9 +56,10 @@ def _dtype(t: torch.Tensor) -> torch.dtype:
 
 
 def _dims(t: torch.Tensor, name: str, n: int):
-    if t.dim() != n:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {n} dimensions")
-    return t.shape
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {n} dimensions")
+    return shape
 
 
 def _ptr(t: torch.Tensor, name: str, shape, dtype, dev) -> int:
@@ -80,15 +81,18 @@ def _workspace(ws: Optional[torch.Tensor], need: int, dev, stream):
             raise ValueError(f"workspace is on {ws.device}, expected {dev}")
         if not ws.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    if need and (ws is None or ws.nbytes < need):
-        ws = _kda._empty((need,), torch.uint8, dev, stream)
-    return (None, None, 0) if ws is None else (ws, ws.data_ptr(), ws.nbytes)
+        if ws.nbytes >= need:
+            return ws, ws.data_ptr(), ws.nbytes
+    if not need:
+        return None, None, 0
+    ws = _kda._empty((need,), torch.uint8, dev, stream)
+    return ws, ws.data_ptr(), need
 
 
 def _call(name: str, dev, stream, *args) -> None:
     fn = getattr(_kda.load_library(), name)
     raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -184,7 +188,8 @@ def kda_attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     pool, Hkv, page, _ = _dims(k_cache, "k_cache", 4)
     B, width = _dims(block_table, "block_table", 2)
     i32, cache = torch.int32, (pool, Hkv, page, d)
-    o = _out(o, (T, Hq, d), dt, dev, stream)
+    if o is None:
+        o = torch.empty_like(q) if stream is None else _kda._empty(q.shape, dt, dev, stream)
     if lse is None and want_lse:
         lse = _kda._empty((T, Hq), torch.float32, dev, stream)
     need = kda_attn_paged_workspace_size(T, B, Hq, Hkv, d, max_new, dt)

@@ -106,7 +106,8 @@ kda_status kda_cache_append(const void* k, const void* v, const int* slot_map,
  *            is empty and the values of rows that two requests claim are
  *            unspecified.
  *   o        [T, Hq, d] in `dtype`; rows outside all requests are left as they
- *            are. A row without any position gives 0.
+ *            are. A row without any position (or with scores of -infinity alone)
+ *            gives 0.
  *   lse      [T, Hq] fp32 or NULL: natural log of the sum of exp(scores),
  *            -infinity for a row without any position
  *   scale    factor on q.k; 0 selects 1 / sqrt(d). Finite, not negative.

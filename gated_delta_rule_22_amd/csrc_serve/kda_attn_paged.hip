@@ -178,10 +178,10 @@ template <int D> __device__ __forceinline__ int v_piece8(int key, int c) {
 }
 
 // The running maximum, sum and rows of 16 RT rows in one wave. Lane l holds
-// row l % 16 of each group of 16 throughout; l is a sum over the lane's own
-// keys until finish().
+// row l % 16 of each group of 16 throughout; the sum stays one over the lane's
+// own keys until the end.
 //
-// bf16: D x 32 keys a step. S^T = K Q^T leaves lane l with the scores of its
+// bf16, 32 keys a step. S^T = K Q^T leaves lane l with the scores of its
 // row against keys 16 sub + 4 (l / 16) + i; as the second operand of
 // O^T += V^T P^T they stay in place when the contraction runs over the keys in
 // that same order, which the transposing LDS read gives V.

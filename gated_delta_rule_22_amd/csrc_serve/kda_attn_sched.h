@@ -10,7 +10,11 @@
 // about 300 instructions up to 256 requests, where a kernel that writes the
 // list first would cost every call a launch. (All four waves doing it spent
 // more time on it than on small calls' keys.) The grid is what the host can
-// bound.
+// bound; workgroups behind the last part end at once.
+//
+// The KV heads of a tile are neighbours in the order of parts: with 8 of them
+// each of the 8 XCDs, which take workgroups in turn, keeps to one head, and
+// the tiles that run there together find its keys in the XCD's own cache.
 #pragma once
 
 #include "kda_serve_launch.h"

@@ -6,15 +6,25 @@
 // place every moved page, and the prefix sum of new_i (cu) every new token.
 //
 // One workgroup checks the inputs, decides the status and scans
-// (page_plan_scan); what is left are three flat lists (slots, pages taken,
-// pages given back), each entry of which finds its request by a binary search
-// in the list's prefix sums (page_plan_fill).
+// (page_plan_scan); what are left are three flat lists (slots, pages taken,
+// pages given back), each entry of which finds its request in the list's prefix
+// sums. For small steps the same workgroup fills them, for others a second
+// launch (page_plan_fill): the counts may be updated in place, so everything
+// has to be read before anything is written. Memory latencies bound both: 256
+// requests of up to 8 tokens 7 us, 1024 requests with 276,000 slots in pages of
+// 16 4.1 + 6 us.
 #include "kda_serve_launch.h"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 1024;
+// One launch up to so many slots and table entries, of which any number may be
+// given back: 256 requests over 259 pages 8.2 us with one, 7.7 with two and
+// another 3 us on the host; 512 over 259 13 and 9; 1024 over 1900, 30% of them
+// ended, 75 and 9.
+constexpr int kOneSlots = 4096;
+constexpr long kOneEntries = 1l << 17;
 
 // Workspace of B requests: pages held before the call (the caller's array
 // may be overwritten in place), prefix sums of pages taken and given back,
@@ -140,11 +150,12 @@ __device__ void fill(const PlanArgs& a, const PlanWs& w, long first, long step) 
     const int B = a.B, mask = (1 << a.page_shift) - 1;
     const int head = w.ring[0], count = w.ring[1];
     const int tokens = a.cu[B], taken = w.taken[B], given = w.given[B];
-    // the slots fill whole waves, so that the lanes of a wave search together
-    const long slots = ((long)a.n_slots + 63) & ~63l;
-    const long all = slots + taken + given;
+    // each list fills whole waves, so that the lanes of a wave search together
+    const auto waves = [](int n) { return ((long)n + 63) & ~63l; };
+    const long taken0 = waves(a.n_slots), given0 = taken0 + waves(taken);
+    const long all = given0 + waves(given);
     for (long j = first; j < all; j += step) {
-        if (j < slots) {
+        if (j < taken0) {
             const int t = (int)j;
             int slot = -1, i = 0;
             // the wave's first slot has a token if any of them has
@@ -158,13 +169,15 @@ __device__ void fill(const PlanArgs& a, const PlanWs& w, long first, long step) 
                 if ((unsigned)page < (unsigned)a.pool) slot = (page << a.page_shift) + (pos & mask);
             }
             if (t < a.n_slots) a.slots[t] = slot;
-        } else if (j < slots + taken) {
-            const int x = (int)(j - slots), i = find(w.taken, B, x);
-            a.table[(long)i * a.width + w.have[i] + (x - w.taken[i])] = a.ring[ring_at(a, head, x)];
+        } else if (j < given0) {
+            const int x = (int)(j - taken0), i = find_wave(w.taken, B, x, x < taken);
+            if (x < taken)
+                a.table[(long)i * a.width + w.have[i] + (x - w.taken[i])] = a.ring[ring_at(a, head, x)];
         } else {
-            const int x = (int)(j - slots - taken), i = find(w.given, B, x);
-            a.ring[ring_at(a, head, count + x)] =
-                a.table[(long)i * a.width + a.pages_out[i] + (x - w.given[i])];
+            const int x = (int)(j - given0), i = find_wave(w.given, B, x, x < given);
+            if (x < given)
+                a.ring[ring_at(a, head, count + x)] =
+                    a.table[(long)i * a.width + a.pages_out[i] + (x - w.given[i])];
         }
     }
 }
@@ -241,11 +254,14 @@ __global__ __launch_bounds__(256) void page_plan_fill(PlanArgs a, void* ws) {
 size_t page_plan_ws(int B) { return (3 * (size_t)B + 4) * sizeof(int); }
 
 hipError_t launch_page_plan(const PlanArgs& a, void* ws, hipStream_t st) {
-    const bool one = a.n_slots <= 4096;
+    const bool one = a.n_slots <= kOneSlots && (long)a.B * a.width <= kOneEntries;
     page_plan_scan<<<1, kThreads, 0, st>>>(a, ws, one);
     if (!one) {
-        const int grid = (int)(((long)a.n_slots + 255) / 256 < 2048 ? ((long)a.n_slots + 255) / 256
-                                                                    : 2048);
+        // a thread per slot, and per page up to 2^17 of them, at most 2^19
+        const long entries = (long)a.B * a.width;
+        long n = (long)a.n_slots + (entries < kOneEntries ? entries : kOneEntries);
+        n = (n + 255) / 256;
+        const int grid = (int)(n < 2048 ? n : 2048);
         page_plan_fill<<<grid, 256, 0, st>>>(a, ws);
     }
     return hipGetLastError();

@@ -195,3 +195,12 @@ def test_many_pages_move_in_a_small_step():
     c = make(31, 300, 16, 2, 6000, gone=0.5)
     c["slots"] = max(c["slots"], sum(c["new"]))
     assert check(c, in_place=True)["status"] == 0
+
+
+@pytest.mark.parametrize("gone", [0.0, 0.6])
+def test_many_pages_over_wide_tables(gone):
+    # more table entries than one workgroup takes, whatever the slots
+    c = make(33, 700, 16, 3, 4000, gone=gone, spare=400)
+    assert 700 * len(c["table"][0]) > 1 << 17 and sum(c["new"]) < 4096
+    assert check(c, in_place=True)["status"] == 0
+    assert check(c)["status"] == 0

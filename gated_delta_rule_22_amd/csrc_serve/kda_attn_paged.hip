@@ -874,6 +874,82 @@ __global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_both_bf16(
     else stream_bf16<D, 2, NT>(a, s1, (int)blockIdx.x - n0, lds.stream);
 }
 
+// The lists of a call of many requests (AttnTable), a workgroup for each of
+// its launches: sixteen waves sum the work and then the parts of their blocks,
+// the first one puts the blocks' sums in order. 4096 requests of one token over
+// 300 positions, 8 KV heads of 128: LISTUS.
+constexpr int kListWaves = 16;
+__global__ __launch_bounds__(64 * kListWaves) void attn_list(AttnArgs a, AttnSplit s0, AttnSplit s1) {
+    __shared__ long cost_of[kListWaves];
+    __shared__ int tiles_of[kListWaves];
+    const AttnSplit& s = blockIdx.x == 0 ? s0 : s1;
+    const AttnTable t(s.table, a.B);
+    const int n = AttnTable::blocks(a.B), wave = wave_id(), lane = threadIdx.x & 63;
+    long cost = 0;
+    int tiles = 0;
+    for (int k = wave; k < n; k += kListWaves) {
+        AttnBlock<false> b;
+        b.load(a, s, k * kBlock);
+        cost += b.cost();
+        tiles += b.tiles();
+    }
+    cost = wave_total(cost);
+    tiles = __builtin_amdgcn_readlane(wave_prefix(tiles), 63);
+    if (lane == 0) {
+        cost_of[wave] = cost;
+        tiles_of[wave] = tiles;
+    }
+    __syncthreads();
+    cost = 0;
+    tiles = 0;
+    for (int w = 0; w < kListWaves; ++w) {
+        cost += cost_of[w];
+        tiles += tiles_of[w];
+    }
+    const int C = attn_part(a, s, cost, tiles);
+    for (int k = wave; k < n; k += kListWaves) {
+        AttnBlock<false> b;
+        b.load(a, s, k * kBlock);
+        b.split(a, C);
+        AttnBlock<true> u = __builtin_bit_cast(AttnBlock<true>, b);
+        u.split(a, C);
+        // (read from lane 63 by the whole wave: the sum's last step must not be
+        // moved to where only lane 0 is active)
+        const int items = b.items(), slots = b.slots(), units = u.items();
+        if (lane == 0) {
+            t.items[k] = items;
+            t.slots[k] = slots;
+            t.units[k] = units;
+        }
+    }
+    __syncthreads();
+    if (wave != 0) return;
+    // in place: each block's own count -> what lies before it
+    int items = 0, slots = 0, units = 0;
+    for (int k = 0; k < n; k += 64) {
+        const bool in = k + lane < n;
+        const int x = in ? t.items[k + lane] : 0, y = in ? t.slots[k + lane] : 0,
+                  z = in ? t.units[k + lane] : 0;
+        const int px = wave_prefix(x), py = wave_prefix(y), pz = wave_prefix(z);
+        if (in) {
+            t.items[k + lane] = items + px - x;
+            t.slots[k + lane] = slots + py - y;
+            t.units[k + lane] = units + pz - z;
+        }
+        items += __builtin_amdgcn_readlane(px, 63);
+        slots += __builtin_amdgcn_readlane(py, 63);
+        units += __builtin_amdgcn_readlane(pz, 63);
+    }
+    if (lane == 0) {
+        t.items[n] = items;
+        t.slots[n] = slots;
+        t.units[n] = units;
+        t.head[0] = C;
+        t.head[1] = items;
+        t.head[2] = units;
+    }
+}
+
 // Joins the parts of tiles that were cut, rows shared evenly by the workgroups.
 // A group of D / 4 lanes holds four columns each of a row. Up to 16 parts every
 // group has a row of its own. With more the groups share one row, each takes
@@ -1068,8 +1144,10 @@ Plan plan_of(int T, int B, int Hq, int Hkv, int d, int max_new, bool bf16_io) {
     }
     // a single request is the tile kernel's whatever its length
     if (p.tiles && B == 1) p.l[0].split.min_rows = 1;
-    for (int i = 0; i < p.n; ++i)
+    for (int i = 0; i < p.n; ++i) {
         p.bytes += (size_t)p.l[i].split.slots * p.l[i].split.R * (d + 2) * sizeof(float);
+        if (B > kBlock) p.bytes += AttnTable::ints(B) * sizeof(int);
+    }
     return p;
 }
 
@@ -1104,6 +1182,7 @@ void launch_stream(const AttnArgs& a, const Plan& p, const Launch& l, hipStream_
 template <int D>
 hipError_t launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
     const Launch &l0 = p.l[0], &l1 = p.l[p.n - 1];
+    if (a.B > kBlock) attn_list<<<(unsigned)p.n, 64 * kListWaves, 0, st>>>(a, l0.split, l1.split);
     if constexpr (D >= 64) {
         const unsigned n0 = (unsigned)l0.items, n = n0 + (unsigned)l1.items;
         if (p.n == 2) {
@@ -1134,6 +1213,10 @@ hipError_t launch_attn_paged(const AttnArgs& a, void* ws, hipStream_t st) {
         s.ml = at;
         s.acc = s.ml + (size_t)s.slots * s.R * 2;
         at = s.acc + (size_t)s.slots * s.R * a.d;
+        if (a.B > kBlock) {
+            s.table = (int*)at;
+            at += AttnTable::ints(a.B);
+        }
     }
     switch (a.d) {
         case 16: return launch<16>(a, p, st);

@@ -7,8 +7,8 @@
 // when few long requests have to fill the card. Lengths are on the
 // device, so the first wave of each workgroup reads them, four requests a
 // lane, sums the work and finds its part in the prefix sums, in registers:
-// about 300 instructions up to 256 requests, where a kernel that writes the
-// list first would cost every call a launch. (All four waves doing it spent
+// about 300 instructions, where a kernel that writes the list first would cost
+// every call a launch. (All four waves doing it spent
 // more time on it than on small calls' keys.) The grid is what the host can
 // bound; workgroups behind the last part end at once.
 //
@@ -28,6 +28,11 @@ constexpr int kAttnThreads = 256;
 // shorter than this for it (a ragged fp32 batch of few keys: 45 us with up to
 // 2048 parts, 32 us with 256).
 constexpr int kLongPart = 1024;
+// Requests that a wave holds, four a lane. With more of them a launch of its
+// own (attn_list) sums the blocks of this many once, and a workgroup reads the
+// sums instead of going through all requests: 1024 requests of one token over
+// 1000 positions 675 -> 4.6 + 640 us, 512 the same.
+constexpr int kBlock = 256;
 
 // What a launch works on, besides AttnArgs.
 struct AttnSplit {
@@ -39,6 +44,7 @@ struct AttnSplit {
     int some_log2;      // more than 2^most_log2, not fewer than 2^some_log2, and as few
     int few_log2;       // as 2^few_log2 rather than parts shorter than kLongPart
     int slots;          // partial results that the workspace holds
+    int* table;         // of more than kBlock requests: see AttnTable; null otherwise
     float* ml;          // [slots][R][2]: running maximum (log2 domain), sum
     float* acc;         // [slots][R][d]: unnormalised rows
 };
@@ -186,63 +192,76 @@ struct AttnBlock {
     }
 };
 
-// The first wave's view of the call. Every workgroup of every kernel of a call
-// computes the same C: the work is summed in whole numbers, and what follows
-// has no product that one compiled kernel could fuse with a sum and another
-// not. The bounds below leave room for its rounding.
+// What attn_list writes down: C, the call's parts and cut tiles, and for every
+// block of kBlock requests what lies before it, with the totals at the end.
+struct AttnTable {
+    int *head, *items, *slots, *units;
+    __host__ __device__ static int blocks(int B) { return (B + kBlock - 1) / kBlock; }
+    __host__ __device__ static size_t ints(int B) {
+        return (size_t)(4 + 3 * ((long)blocks(B) + 1) + 3) & ~(size_t)3;
+    }
+    __device__ AttnTable(int* t, int B)
+        : head(t), items(t + 4), slots(items + blocks(B) + 1), units(slots + blocks(B) + 1) {}
+};
+
+// Keys of a part from the call's work and tiles. What follows the sums (whole
+// numbers) has no product that one compiled kernel could fuse with a sum and
+// another not: every workgroup of every kernel of a call gets the same C. The
+// bounds below leave room for its rounding.
+__device__ __forceinline__ int attn_part(const AttnArgs& a, const AttnSplit& s, long cost, int tiles) {
+    const float total = (float)(cost * a.Hkv), all = (float)(tiles * a.Hkv);
+    const float parts = fminf(fmaxf(all, (float)(1 << s.some_log2)), (float)(1 << s.most_log2));
+    const float most = total / parts;
+    const float few = total * __builtin_bit_cast(float, (127 - s.few_log2) << 23);
+    const float want = fmaxf(most, fminf(few, (float)kLongPart));
+    // a part covers at most all positions
+    return __builtin_amdgcn_readfirstlane(((int)fminf(want, 1073741824.f) & ~(s.unit - 1)) + s.unit);
+}
+
+// The first wave's view of the call: one block of requests at a time, the only
+// one of a call of up to kBlock.
 template <bool UNITS>
 struct AttnSched {
-    AttnBlock<UNITS> first;
+    AttnBlock<UNITS> block;
     int C, items;
 
     __device__ void init(const AttnArgs& a, const AttnSplit& s) {
-        first.load(a, s, 0);
-        long cost = first.cost();
-        int tiles = first.tiles();
-        for (int base = 256; base < a.B; base += 256) {
-            AttnBlock<UNITS> b;
-            b.load(a, s, base);
-            cost += b.cost();
-            tiles += b.tiles();
-        }
-        const float total = (float)(wave_total(cost) * a.Hkv);
-        const float all = (float)(__builtin_amdgcn_readlane(wave_prefix(tiles), 63) * a.Hkv);
-        const float parts = fminf(fmaxf(all, (float)(1 << s.some_log2)), (float)(1 << s.most_log2));
-        const float most = total / parts;
-        const float few = total * __builtin_bit_cast(float, (127 - s.few_log2) << 23);
-        const float want = fmaxf(most, fminf(few, (float)kLongPart));
-        // a part covers at most all positions
-        C = __builtin_amdgcn_readfirstlane(((int)fminf(want, 1073741824.f) & ~(s.unit - 1)) + s.unit);
-        first.split(a, C);
-        items = first.items();
-        if (UNITS)
-            for (int base = 256; base < a.B; base += 256) {
-                AttnBlock<UNITS> b;
-                b.load(a, s, base);
-                b.split(a, C);
-                items += b.items();
-            }
-    }
-    // The y-th item of the call into LDS; found = false behind the last.
-    __device__ void find(const AttnArgs& a, const AttnSplit& s, int y, AttnItem* to) const {
-        if (threadIdx.x == 0) to->found = false;
-        int at = first.items(), slot0 = first.slots();
-        if (y < at) {
-            first.find(a, 0, y, 0, C, to);
+        if (s.table) {
+            C = __builtin_amdgcn_readfirstlane(s.table[0]);
+            items = __builtin_amdgcn_readfirstlane(s.table[UNITS ? 2 : 1]);
             return;
         }
-        for (int base = 256; base < a.B; base += 256) {
-            AttnBlock<UNITS> b;
-            b.load(a, s, base);
-            b.split(a, C);
-            const int n = b.items();
-            if (y < at + n) {
-                b.find(a, base, y - at, slot0, C, to);
-                return;
+        block.load(a, s, 0);
+        C = attn_part(a, s, wave_total(block.cost()),
+                      __builtin_amdgcn_readlane(wave_prefix(block.tiles()), 63));
+        block.split(a, C);
+        items = block.items();
+    }
+    // The y-th item of the call into LDS; found = false behind the last.
+    __device__ void find(const AttnArgs& a, const AttnSplit& s, int y, AttnItem* to) {
+        if (threadIdx.x == 0) to->found = false;
+        if (y >= items) return;
+        int base = 0, before = 0, slot0 = 0;
+        if (s.table) {
+            const AttnTable t(s.table, a.B);
+            const int* list = UNITS ? t.units : t.items;
+            const int n = AttnTable::blocks(a.B), lane = threadIdx.x & 63;
+            // the block whose successor begins behind y
+            int k = 0;
+            unsigned long long behind = 0;
+            for (; k < n; k += 64) {
+                behind = __ballot(list[min(k + lane, n - 1) + 1] > y);
+                if (behind) break;
             }
-            at += n;
-            slot0 += b.slots();
+            if (!behind) return;
+            k += __builtin_ctzll(behind);
+            base = k * kBlock;
+            before = list[k];
+            slot0 = t.slots[k];
+            block.load(a, s, base);
+            block.split(a, C);
         }
+        block.find(a, base, y - before, slot0, C, to);
     }
 };
 

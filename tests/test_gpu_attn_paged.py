@@ -255,12 +255,16 @@ def test_cache_past_32_bit_offsets():
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("B", [300, 1100])
+@pytest.mark.parametrize("B", [256, 257, 300, 1100, 17000])
 def test_many_requests(B, dtype):
     n = [(i * 7) % 4 for i in range(B)]
     ctx = [(i * 131) % 90 for i in range(B)]
-    n[B // 2], ctx[3] = 70, 3000
-    check(R.attn_case(n, ctx, 2, 1, 64, 16, dtype, seed=58))
+    if B > 5000:                                     # more than 64 blocks of requests
+        n = [x if i % 16 == 0 else 0 for i, x in enumerate(n)]
+        ctx = [x if i % 16 == 0 else 0 for i, x in enumerate(ctx)]
+    n[B // 2], ctx[3], n[3], n[B - 1], ctx[B - 1] = 70, 3000, 1, 2, 700
+    for hint in (0, 2):
+        check(R.attn_case(n, ctx, 2, 1, 64, 16, dtype, seed=58), max_new=hint)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])

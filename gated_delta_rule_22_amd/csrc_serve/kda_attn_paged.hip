@@ -13,9 +13,9 @@
 // (fp32: 16) keys each in turn and run free of each other, so that every wave
 // has its next keys and values in flight while it computes. Their rows are
 // joined through LDS at the end. bf16, 32 query heads over 8 of 128: one token
-// of 256 requests over 1024 to 16384 positions (5.8 GB) 965 + 7 us, 6.0 TB/s;
+// of 256 requests over 1024 to 16384 positions (5.8 GB) 970 + 7 us, 6.0 TB/s;
 // 8 tokens of 4 over 65536 to 262144 (2.6 GB) 425 + 8 us, 6.2 TB/s; one token
-// over 1000 positions 7.5 + 4.3 us, all of it latency. fp32, 16 heads over 4:
+// over 1000 positions 8.4 + 4.3 us, all of it latency. fp32, 16 heads over 4:
 // 64 tokens over 4096 positions (1.1 GB) 200 us, 5.4 TB/s; 1024 tokens over
 // 1024 of width 64 83 us, half of the fp32 matrix rate.
 #include "kda_attn_sched.h"

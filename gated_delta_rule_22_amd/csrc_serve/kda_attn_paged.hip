@@ -877,7 +877,8 @@ __global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_both_bf16(
 // The lists of a call of many requests (AttnTable), a workgroup for each of
 // its launches: sixteen waves sum the work and then the parts of their blocks,
 // the first one puts the blocks' sums in order. 4096 requests of one token over
-// 300 positions, 8 KV heads of 128: LISTUS.
+// 300 positions, 8 KV heads of 128: 8.0 us (1024 requests: 5.0), memory
+// latencies of two passes over the lengths, which stay in the cache for the second.
 constexpr int kListWaves = 16;
 __global__ __launch_bounds__(64 * kListWaves) void attn_list(AttnArgs a, AttnSplit s0, AttnSplit s1) {
     __shared__ long cost_of[kListWaves];

@@ -55,6 +55,27 @@ __device__ __forceinline__ f32x4 mma4(float a, float b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
+// Eight weights p >= 0 as two bf16 terms each: the leading bits cut off, and what
+// is left of p (1 + 2^-20). One term would lose up to 2^-8 of a weight, as much
+// as the result's own rounding does (2.0e-3 to 2.3e-3 from fp64 in all instead of
+// 1.7e-3); two lose 2^-15 (1.7e-3 in all). The second one's products cost the
+// streams nothing and prompts a quarter to a third: 8192 tokens over 24576
+// positions, 32 heads over 8 of 128, 4.0 -> 5.3 ms, 4096 over 12000 of width 64
+// 0.66 -> 0.83 ms. The 2^-20 keeps the second term of p > 0 above 0, so
+// that both have the sign of p and an infinite value stays infinite.
+__device__ __forceinline__ void two_terms(const float (&p)[8], bf16x8& hi, bf16x8& lo) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4 h;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const uint32_t a = __builtin_bit_cast(uint32_t, p[j]), b = __builtin_bit_cast(uint32_t, p[j + 1]);
+        h[j / 2] = __builtin_amdgcn_perm(b, a, 0x07060302);      // upper halves
+        lo[j] = (bf16)__builtin_fmaf(p[j], 1.f + 0x1p-20f, -__builtin_bit_cast(float, a & 0xffff0000u));
+        lo[j + 1] = (bf16)__builtin_fmaf(p[j + 1], 1.f + 0x1p-20f, -__builtin_bit_cast(float, b & 0xffff0000u));
+    }
+    hi = __builtin_bit_cast(bf16x8, h);
+}
+
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // Largest over the four lanes l % 16 + {0, 16, 32, 48}.
@@ -319,7 +340,7 @@ __device__ __forceinline__ void stream_bf16(const AttnArgs& a, const AttnSplit& 
         }
         page_next[0] = page_2;
         page_next[1] = page_3;
-        bf16x8 pf[RT];
+        bf16x8 pf[RT], pr[RT];
         float pe[RT][2][4];
         for (int rt = 0; rt < RT; ++rt) {
             float x[2][4];
@@ -351,10 +372,8 @@ __device__ __forceinline__ void stream_bf16(const AttnArgs& a, const AttnSplit& 
                     pe[rt][u][i] = p;
                 }
             l[rt] += sum;
-            // the weights are rounded to bf16 for the matrix cores (at most 2^-8 each,
-            // see the test bounds); l sums them unrounded
-            pf[rt] = pack8(f32x4{pe[rt][0][0], pe[rt][0][1], pe[rt][0][2], pe[rt][0][3]},
-                           f32x4{pe[rt][1][0], pe[rt][1][1], pe[rt][1][2], pe[rt][1][3]});
+            two_terms({pe[rt][0][0], pe[rt][0][1], pe[rt][0][2], pe[rt][0][3], pe[rt][1][0],
+                       pe[rt][1][1], pe[rt][1][2], pe[rt][1][3]}, pf[rt], pr[rt]);
         }
         lds_fence_wave();                            // the stage is written
         for (int b = 0; b < NB; ++b) {
@@ -366,7 +385,10 @@ __device__ __forceinline__ void stream_bf16(const AttnArgs& a, const AttnSplit& 
                 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(x + 16 * D));
             }
             const bf16x8 va = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-            for (int rt = 0; rt < RT; ++rt) acc[rt][b] = mma32(va, pf[rt], acc[rt][b]);
+            for (int rt = 0; rt < RT; ++rt) {
+                acc[rt][b] = mma32(va, pf[rt], acc[rt][b]);
+                acc[rt][b] = mma32(va, pr[rt], acc[rt][b]);
+            }
         }
         if (odd) {
             // the values left out above, for the rows that see them
@@ -596,10 +618,10 @@ __device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, const voi
 }
 
 // Prompts: tiles of 128 rows, 32 per wave, against 64 keys at a time that all
-// waves share in LDS. What bounds it is the matrix cores, 4 D flops per row
-// and key, the LDS reads that feed them (each wave reads all 64 keys and
-// values for its 32 rows: 32 cycles a product, as long as the product takes),
-// and the exponentials.
+// waves share in LDS. What bounds it is the matrix cores, 6 D flops per row
+// and key (4 D of the definition and 2 D of the weights' second terms), the LDS
+// reads that feed them (each wave reads all 64 keys and values for its 32
+// rows), and the exponentials.
 //
 // As above S^T = K Q^T and O^T += V^T P^T, with the 32x32x16 product: the
 // scores of row l % 32 stay in lanes l and l + 32 and are the second operand
@@ -607,10 +629,10 @@ __device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, const voi
 // while the exponentials of these run, so that the matrix cores have work in
 // both; K is therefore fetched two steps ahead and V one, two buffers each.
 //
-// 8192 tokens over 24576 positions, 32 heads over 8 of 128: 3.6 to 3.95 ms
-// from card to card, 0.98 to 1.06 PFLOP/s, with the matrix cores busy 46% of
-// the cycles at 2.0 GHz: the clock falls as they fill, and a library product
-// of 8192^3 reaches 1.20 PFLOP/s there. (Scores of the next 64 keys made while
+// 8192 tokens over 24576 positions, 32 heads over 8 of 128: 5.2 to 5.4 ms
+// from card to card, 5.8 TFLOP of products at 1.07 to 1.11 PFLOP/s; the clock
+// falls as the matrix cores fill, and a library product of 8192^3 reaches 1.20
+// PFLOP/s there. (Before the second terms: scores of the next 64 keys made while
 // the exponentials of these run, K fetched two steps ahead: the same at width
 // 128, 8% longer at 64, where the registers leave a workgroup less.)
 //
@@ -767,7 +789,7 @@ __device__ __forceinline__ void tile_bf16(const AttnArgs& a, const AttnSplit& s,
         scores(kt, st);
         settle(st, pos, missing);
         const float mu = m == -INFINITY ? 0.f : m;
-        bf16x8 pf[4];
+        bf16x8 pf[4], pr[4];
         float sum = 0.f;
         for (int u = 0; u < 2; ++u)
             for (int i = 0; i < 16; ++i) {
@@ -776,9 +798,11 @@ __device__ __forceinline__ void tile_bf16(const AttnArgs& a, const AttnSplit& s,
                 st[u][i] = p;
             }
         l += sum;
-        // the weights are rounded to bf16 for the matrix cores; l sums them unrounded
-        for (int ks = 0; ks < 4; ++ks)
-            for (int j = 0; j < 8; ++j) pf[ks][j] = (bf16)st[ks / 2][8 * (ks % 2) + j];
+        for (int ks = 0; ks < 4; ++ks) {
+            float p[8];
+            for (int j = 0; j < 8; ++j) p[j] = st[ks / 2][8 * (ks % 2) + j];
+            two_terms(p, pf[ks], pr[ks]);
+        }
         for (int ks = 0; ks < 4; ++ks)
             for (int b = 0; b < NB; ++b) {
                 s16x4 x[2];
@@ -791,6 +815,7 @@ __device__ __forceinline__ void tile_bf16(const AttnArgs& a, const AttnSplit& s,
                 }
                 const bf16x8 va = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
                 acc[b] = mma_big(va, pf[ks], acc[b]);
+                acc[b] = mma_big(va, pr[ks], acc[b]);
             }
         if (odd) {
             // the values left out above, for the rows that see them

@@ -20,6 +20,8 @@
 // 1024 of width 64 83 us, half of the fp32 matrix rate.
 #include "kda_attn_sched.h"
 
+#include <limits.h>
+
 namespace kda {
 namespace {
 
@@ -213,14 +215,12 @@ template <int D> struct StreamLds {
     AttnItem item;
 };
 template <int D, int RT, bool NT>
-__device__ __forceinline__ void stream_bf16(const AttnArgs& a, const AttnSplit& s, int block,
-                                            StreamLds<D>& lds) {
+__device__ __forceinline__ void stream_part(const AttnArgs& a, const AttnSplit& s,
+                                            const AttnItem& it, StreamLds<D>& lds) {
     constexpr int KS = D < 32 ? 1 : D / 32;          // steps of 32 over the head
     constexpr int NB = D / 16;                       // value columns in 16s
     constexpr int VL = D / 16;                       // 16-byte loads per lane for 32 rows of V
     constexpr int CH = D / 8;                        // 16-byte pieces of a row
-    const AttnItem it = attn_item(a, s, block, lds.item);
-    if (!it.found) return;
     const int G = a.Hq / a.Hkv, wave = wave_id(), lane = threadIdx.x & 63;
     const int c16 = lane & 15, g4 = lane >> 4;
     const Keys keys = part_keys(a, s, it, G);
@@ -426,10 +426,25 @@ __device__ __forceinline__ void stream_bf16(const AttnArgs& a, const AttnSplit& 
         join_waves<bf16, D>(a, s, it, G, rt * 16, lds.join_ml, lds.join);
     }
 }
-template <int D, int RT, bool NT>
+// Keys and values that are read once, and are more than the last-level cache
+// holds, are read past it (see far_keys).
+template <int D, int RT>
+__device__ __forceinline__ void stream_bf16(const AttnArgs& a, const AttnSplit& s, int block,
+                                            StreamLds<D>& lds) {
+    const AttnItem it = attn_item(a, s, block, lds.item);
+    if (!it.found) return;
+    if constexpr (D >= 64) {
+        if (it.far) {
+            stream_part<D, RT, true>(a, s, it, lds);
+            return;
+        }
+    }
+    stream_part<D, RT, false>(a, s, it, lds);
+}
+template <int D, int RT>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, AttnSplit s) {
     __shared__ StreamLds<D> lds;
-    stream_bf16<D, RT, NT>(a, s, (int)blockIdx.x, lds);
+    stream_bf16<D, RT>(a, s, (int)blockIdx.x, lds);
 }
 
 // fp32, 16 keys a step. The contraction over the head takes element
@@ -886,7 +901,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_tile_bf16(
 // Long and short requests of a call at once: the first n0 workgroups are the
 // tiles', the others the streams'. Two launches took the longer of the two
 // plus the other (25 + 13 us in a ragged batch).
-template <int D, bool NT>
+template <int D>
 __global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_both_bf16(AttnArgs a, AttnSplit s0,
                                                                   AttnSplit s1, int n0) {
     union Lds {
@@ -896,7 +911,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_both_bf16(
     };
     __shared__ Lds lds;
     if ((int)blockIdx.x < n0) tile_bf16<D>(a, s0, (int)blockIdx.x, lds.tile);
-    else stream_bf16<D, 2, NT>(a, s1, (int)blockIdx.x - n0, lds.stream);
+    else stream_bf16<D, 2>(a, s1, (int)blockIdx.x - n0, lds.stream);
 }
 
 // The lists of a call of many requests (AttnTable), a workgroup for each of
@@ -973,6 +988,7 @@ __global__ __launch_bounds__(64 * kListWaves) void attn_list(AttnArgs a, AttnSpl
         t.head[0] = C;
         t.head[1] = items;
         t.head[2] = units;
+        t.head[3] = cost > s.far;
     }
 }
 
@@ -1177,28 +1193,26 @@ Plan plan_of(int T, int B, int Hq, int Hkv, int d, int max_new, bool bf16_io) {
     return p;
 }
 
-// Whether K and V of the pool are past what the last-level cache (256 MB) may
-// still hold of them from an earlier call. Then the stream kernel for bf16, d
-// of 64 and 128 reads them non-temporally (there a request is one tile, so
-// nothing is read twice): decode batch over 5.8 GB 1017 -> 971 us. Over a pool
-// of 250 MB that repeated calls find in the cache it costs 47 -> 60 us.
-bool past_cache(const AttnArgs& a) {
-    return ((size_t)a.pool << a.page_shift) * a.Hkv * a.d * 4 > (size_t)512 << 20;
+// Keys of a call (times tiles that read them) above which the stream kernel for
+// bf16, d of 64 and 128 reads K and V non-temporally, where a request is one
+// tile and so reads them once: 512 MB of them, twice what the last-level cache
+// could still hold from an earlier call, and only of a pool that is larger
+// itself (requests may share pages). Decode batch over 5.8 GB 1017 -> 971 us.
+// 201 MB that repeated calls find in the cache, of a pool of 17 GB, read so: 42
+// -> 51 us (16 requests of one token over 3000 positions, 32 heads over 8 of 128).
+long far_keys(const AttnArgs& a) {
+    constexpr size_t kFarBytes = (size_t)512 << 20;
+    const size_t key = (size_t)a.Hkv * a.d * 4;      // bytes of K and V
+    if (!a.bf16_io || a.d < 64 || ((size_t)a.pool << a.page_shift) * key <= kFarBytes) return LONG_MAX;
+    return (long)(kFarBytes / key);
 }
 
 template <int D>
 void launch_stream(const AttnArgs& a, const Plan& p, const Launch& l, hipStream_t st) {
     const unsigned grid = (unsigned)l.items;
     if (a.bf16_io) {
-        if constexpr (D >= 64) {
-            if (past_cache(a)) {
-                if (p.RT == 1) attn_stream_bf16<D, 1, true><<<grid, kAttnThreads, 0, st>>>(a, l.split);
-                else attn_stream_bf16<D, 2, true><<<grid, kAttnThreads, 0, st>>>(a, l.split);
-                return;
-            }
-        }
-        if (p.RT == 1) attn_stream_bf16<D, 1, false><<<grid, kAttnThreads, 0, st>>>(a, l.split);
-        else attn_stream_bf16<D, 2, false><<<grid, kAttnThreads, 0, st>>>(a, l.split);
+        if (p.RT == 1) attn_stream_bf16<D, 1><<<grid, kAttnThreads, 0, st>>>(a, l.split);
+        else attn_stream_bf16<D, 2><<<grid, kAttnThreads, 0, st>>>(a, l.split);
     } else {
         if (p.RT == 1) attn_stream_f32<D, 1><<<grid, kAttnThreads, 0, st>>>(a, l.split);
         else attn_stream_f32<D, 2><<<grid, kAttnThreads, 0, st>>>(a, l.split);
@@ -1212,8 +1226,7 @@ hipError_t launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
     if constexpr (D >= 64) {
         const unsigned n0 = (unsigned)l0.items, n = n0 + (unsigned)l1.items;
         if (p.n == 2) {
-            if (past_cache(a)) attn_both_bf16<D, true><<<n, kAttnThreads, 0, st>>>(a, l0.split, l1.split, (int)n0);
-            else attn_both_bf16<D, false><<<n, kAttnThreads, 0, st>>>(a, l0.split, l1.split, (int)n0);
+            attn_both_bf16<D><<<n, kAttnThreads, 0, st>>>(a, l0.split, l1.split, (int)n0);
         } else if (p.tiles) {
             attn_tile_bf16<D><<<n0, kAttnThreads, 0, st>>>(a, l0.split);
         }
@@ -1236,6 +1249,7 @@ hipError_t launch_attn_paged(const AttnArgs& a, void* ws, hipStream_t st) {
     float* at = (float*)ws;
     for (int i = 0; i < p.n; ++i) {
         AttnSplit& s = p.l[i].split;
+        s.far = far_keys(a);
         s.ml = at;
         s.acc = s.ml + (size_t)s.slots * s.R * 2;
         at = s.acc + (size_t)s.slots * s.R * a.d;

@@ -43,6 +43,8 @@ struct AttnSplit {
     int most_log2;      // parts over the whole call: about as many as tiles, but not
     int some_log2;      // more than 2^most_log2, not fewer than 2^some_log2, and as few
     int few_log2;       // as 2^few_log2 rather than parts shorter than kLongPart
+    long far;           // keys of all tiles above which the cache is read past the last
+                        // level (see far_keys)
     int slots;          // partial results that the workspace holds
     int* table;         // of more than kBlock requests: see AttnTable; null otherwise
     float* ml;          // [slots][R][2]: running maximum (log2 domain), sum
@@ -56,6 +58,7 @@ struct AttnItem {
     int kept;           // its tokens before them
     int C;              // keys of a part
     int slot;           // partial result of part 0, tile 0, head 0
+    bool far;           // its keys and values are read once, and more than a cache holds
     bool found;
 };
 
@@ -167,7 +170,8 @@ struct AttnBlock {
     __device__ int items() const { return __builtin_amdgcn_readlane(p, 63); }
     __device__ int slots() const { return __builtin_amdgcn_readlane(q, 63); }
     // Item y of these, 0 <= y < items(): the lane that has it writes it down.
-    __device__ void find(const AttnArgs& a, int base, int y, int slot0, int C, AttnItem* to) const {
+    __device__ void find(const AttnArgs& a, int base, int y, int slot0, int C, bool far,
+                         AttnItem* to) const {
         const int local = y - (p - mine);
         if (local < 0 || local >= mine) return;
         // (a request without items begins where the next one does)
@@ -188,12 +192,14 @@ struct AttnBlock {
         to->kept = of(r0.kept, r1.kept, r2.kept, r3.kept);
         to->C = C;
         to->slot = slot0 + q - cut + of(0, c1, c2, c3);
+        to->far = far && tiles == 1;
         to->found = tiles > 0 && (int)part < n;
     }
 };
 
-// What attn_list writes down: C, the call's parts and cut tiles, and for every
-// block of kBlock requests what lies before it, with the totals at the end.
+// What attn_list writes down: C, the call's parts and cut tiles, whether its
+// keys are more than a cache holds, and for every block of kBlock requests what
+// lies before it, with the totals at the end.
 struct AttnTable {
     int *head, *items, *slots, *units;
     __host__ __device__ static int blocks(int B) { return (B + kBlock - 1) / kBlock; }
@@ -224,16 +230,19 @@ template <bool UNITS>
 struct AttnSched {
     AttnBlock<UNITS> block;
     int C, items;
+    bool far;
 
     __device__ void init(const AttnArgs& a, const AttnSplit& s) {
         if (s.table) {
             C = __builtin_amdgcn_readfirstlane(s.table[0]);
             items = __builtin_amdgcn_readfirstlane(s.table[UNITS ? 2 : 1]);
+            far = __builtin_amdgcn_readfirstlane(s.table[3]) != 0;
             return;
         }
         block.load(a, s, 0);
-        C = attn_part(a, s, wave_total(block.cost()),
-                      __builtin_amdgcn_readlane(wave_prefix(block.tiles()), 63));
+        const long cost = wave_total(block.cost());
+        C = attn_part(a, s, cost, __builtin_amdgcn_readlane(wave_prefix(block.tiles()), 63));
+        far = cost > s.far;
         block.split(a, C);
         items = block.items();
     }
@@ -261,7 +270,7 @@ struct AttnSched {
             block.load(a, s, base);
             block.split(a, C);
         }
-        block.find(a, base, y - before, slot0, C, to);
+        block.find(a, base, y - before, slot0, C, far, to);
     }
 };
 
@@ -280,6 +289,7 @@ __device__ __forceinline__ AttnItem attn_shared(const AttnItem& lds) {
     it.kept = __builtin_amdgcn_readfirstlane(it.kept);
     it.C = __builtin_amdgcn_readfirstlane(it.C);
     it.slot = __builtin_amdgcn_readfirstlane(it.slot);
+    it.far = __builtin_amdgcn_readfirstlane((int)it.far) != 0;
     it.found = __builtin_amdgcn_readfirstlane((int)it.found) != 0;
     return it;
 }

@@ -137,7 +137,7 @@ __device__ __forceinline__ void join_waves(const AttnArgs& a, const AttnSplit& s
     const int r = it.tile * s.R + r0 + row;
     if (it.parts > 1) {
         const long slot = (long)it.slot + ((long)it.part * it.tiles + it.tile) * a.Hkv + it.h;
-        if ((unsigned long)slot >= (unsigned long)s.slots) return;   // only where offsets decrease
+        if ((unsigned long)slot >= (unsigned long)s.slots) return;   // (a guard)
         const long at = slot * s.R + r0 + row;
         // (a row without a key in this part has l = 0, and its values are not read)
         for (int i = 0; l != 0.f && i < kPer; i += 4)
@@ -867,7 +867,7 @@ __device__ __forceinline__ void tile_bf16(const AttnArgs& a, const AttnSplit& s,
     const int row = wave * 32 + c32;
     if (it.parts > 1) {
         const long slot = (long)it.slot + ((long)it.part * it.tiles + it.tile) * a.Hkv + it.h;
-        if ((unsigned long)slot >= (unsigned long)s.slots) return;   // only where offsets decrease
+        if ((unsigned long)slot >= (unsigned long)s.slots) return;   // (a guard)
         float* x = s.acc + (slot * s.R + row) * D;
         // (a row without a key in this part has l = 0, and its values are not read)
         for (int b = 0; sum != 0.f && b < NB; ++b)
@@ -921,30 +921,34 @@ __global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_both_bf16(
 // latencies of two passes over the lengths, which stay in the cache for the second.
 constexpr int kListWaves = 16;
 __global__ __launch_bounds__(64 * kListWaves) void attn_list(AttnArgs a, AttnSplit s0, AttnSplit s1) {
-    __shared__ long cost_of[kListWaves];
+    __shared__ long cost_of[kListWaves], claims_of[kListWaves];
     __shared__ int tiles_of[kListWaves];
     const AttnSplit& s = blockIdx.x == 0 ? s0 : s1;
     const AttnTable t(s.table, a.B);
     const int n = AttnTable::blocks(a.B), wave = wave_id(), lane = threadIdx.x & 63;
-    long cost = 0;
+    long cost = 0, claims = 0;
     int tiles = 0;
     for (int k = wave; k < n; k += kListWaves) {
         AttnBlock<false> b;
         b.load(a, s, k * kBlock);
         cost += b.cost();
+        claims += b.claims();
         tiles += b.tiles();
     }
     cost = wave_total(cost);
+    claims = wave_total(claims);
     tiles = __builtin_amdgcn_readlane(wave_prefix(tiles), 63);
     if (lane == 0) {
         cost_of[wave] = cost;
+        claims_of[wave] = claims;
         tiles_of[wave] = tiles;
     }
     __syncthreads();
-    cost = 0;
+    cost = claims = 0;
     tiles = 0;
     for (int w = 0; w < kListWaves; ++w) {
         cost += cost_of[w];
+        claims += claims_of[w];
         tiles += tiles_of[w];
     }
     const int C = attn_part(a, s, cost, tiles);
@@ -986,8 +990,8 @@ __global__ __launch_bounds__(64 * kListWaves) void attn_list(AttnArgs a, AttnSpl
         t.slots[n] = slots;
         t.units[n] = units;
         t.head[0] = C;
-        t.head[1] = items;
-        t.head[2] = units;
+        t.head[1] = claims > a.T ? 0 : items;
+        t.head[2] = claims > a.T ? 0 : units;
         t.head[3] = cost > s.far;
     }
 }
@@ -1030,8 +1034,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit 
         if (threadIdx.x == 0) shared_units = sched.items;
     }
     __syncthreads();
-    // an even share of the rows of all cut tiles (more of them than partial
-    // results there are only where offsets decrease)
+    // an even share of the rows of all cut tiles, of which the partial results
+    // are two or more each
     const unsigned all = (unsigned)min(max(uniform(shared_units), 0), s.slots) << s.R_log2;
     const unsigned share = (all + blocks - 1) / blocks;
     const unsigned row_end = min(all, share * (block + 1));
@@ -1043,7 +1047,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit 
         const int rows = (int)min((unsigned)(s.R - row0), row_end - r);
         r += rows;
         const int step = it.tiles * a.Hkv, slot = it.slot + it.tile * a.Hkv + it.h;
-        // (only where offsets decrease)
+        // (a guard)
         if (!it.found || slot < 0 || slot + (long)step * (it.parts - 1) >= s.slots) continue;
         const int have = min(rows, it.n * G - (it.tile * s.R + row0));   // rows that exist
         auto part = [&](int row, int p) {

@@ -62,7 +62,7 @@ struct AttnItem {
     bool found;
 };
 
-struct AttnReq { int n, kv, tiles, row0, kept; };
+struct AttnReq { int n, kv, tiles, row0, kept; bool back; };
 
 // A request from its offsets and length as they are stored; in = false: none.
 __device__ __forceinline__ AttnReq attn_req(const AttnArgs& a, const AttnSplit& s, bool in, int lo,
@@ -73,6 +73,7 @@ __device__ __forceinline__ AttnReq attn_req(const AttnArgs& a, const AttnSplit& 
     const int cap = a.width << a.page_shift;         // at most 2^30, as T is
     r.row0 = lo;
     r.n = in ? max(hi - lo, 0) : 0;
+    r.back = in && hi < lo;
     r.kept = min(max(kept, 0), cap);
     r.kv = r.kept + min(r.n, cap - r.kept);
     const int rows = r.n * (a.Hq / a.Hkv);           // at most T Hq
@@ -133,6 +134,11 @@ struct AttnBlock {
         r3 = attn_req(a, s, i + 3 <= last, u3, u4, k3);
     }
     __device__ int tiles() const { return r0.tiles + r1.tiles + (r2.tiles + r3.tiles); }
+    // Rows that the requests claim. More than T of them in a call (some twice,
+    // which takes offsets that decrease) would be more tiles than the grid and
+    // the workspace are made for: such a call has no items.
+    __device__ bool back() const { return r0.back || r1.back || r2.back || r3.back; }
+    __device__ long claims() const { return (long)r0.n + r1.n + ((long)r2.n + r3.n); }
     __device__ long cost() const {
         return (long)r0.tiles * r0.kv + (long)r1.tiles * r1.kv +
                ((long)r2.tiles * r2.kv + (long)r3.tiles * r3.kv);
@@ -245,6 +251,7 @@ struct AttnSched {
         far = cost > s.far;
         block.split(a, C);
         items = block.items();
+        if (__any(block.back()) && wave_total(block.claims()) > a.T) items = 0;
     }
     // The y-th item of the call into LDS; found = false behind the last.
     __device__ void find(const AttnArgs& a, const AttnSplit& s, int y, AttnItem* to) {

@@ -103,8 +103,9 @@ kda_status kda_cache_append(const void* k, const void* v, const int* slot_map,
  *            past max_pages * page_size or in a page outside [0, n_pool) are
  *            treated as masked. cu_new is meant to be non-decreasing inside
  *            [0, T]; it is clamped there, and where it decreases the request
- *            is empty and the values of rows that two requests claim are
- *            unspecified.
+ *            is empty. The values of rows that two requests claim are
+ *            unspecified; requests that claim more than T rows together make
+ *            the call an empty one, which writes no row.
  *   o        [T, Hq, d] in `dtype`; rows outside all requests are left as they
  *            are. A row without any position (or with scores of -infinity alone)
  *            gives 0.

@@ -442,9 +442,10 @@ __device__ __forceinline__ void stream_bf16(const AttnArgs& a, const AttnSplit& 
     stream_part<D, RT, false>(a, s, it, lds);
 }
 template <int D, int RT>
-__global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, AttnSplit s) {
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, AttnSplit s,
+                                                                    unsigned first) {
     __shared__ StreamLds<D> lds;
-    stream_bf16<D, RT>(a, s, (int)blockIdx.x, lds);
+    stream_bf16<D, RT>(a, s, (int)(first + blockIdx.x), lds);
 }
 
 // fp32, 16 keys a step. The contraction over the head takes element
@@ -452,12 +453,13 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_bf16(AttnArgs a, 
 // is contiguous; O^T's row 4 g + i of block c is value column (4 g + i) D / 16
 // + c, so that a lane's part of a value row is contiguous too.
 template <int D, int RT>
-__global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_f32(AttnArgs a, AttnSplit s) {
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_stream_f32(AttnArgs a, AttnSplit s,
+                                                                   unsigned first) {
     constexpr int KD = D / 4, NB = D / 16;
     __shared__ __align__(16) float join[4 * 16 * (D + 4)];
     __shared__ float join_ml[4 * 16 * 2];
     __shared__ AttnItem shared_item;
-    const AttnItem it = attn_item(a, s, (int)blockIdx.x, shared_item);
+    const AttnItem it = attn_item(a, s, (int)(first + blockIdx.x), shared_item);
     if (!it.found) return;
     const int G = a.Hq / a.Hkv, wave = wave_id(), lane = threadIdx.x & 63;
     const int c16 = lane & 15, g4 = lane >> 4;
@@ -893,9 +895,10 @@ __device__ __forceinline__ void tile_bf16(const AttnArgs& a, const AttnSplit& s,
 }
 
 template <int D>
-__global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_tile_bf16(AttnArgs a, AttnSplit s) {
+__global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_tile_bf16(AttnArgs a, AttnSplit s,
+                                                                               unsigned first) {
     __shared__ TileLds<D> lds;
-    tile_bf16<D>(a, s, (int)blockIdx.x, lds);
+    tile_bf16<D>(a, s, (int)(first + blockIdx.x), lds);
 }
 
 // Long and short requests of a call at once: the first n0 workgroups are the
@@ -903,15 +906,17 @@ __global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_tile_bf16(
 // plus the other (25 + 13 us in a ragged batch).
 template <int D>
 __global__ __launch_bounds__(kAttnThreads, D == 64 ? 3 : 2) void attn_both_bf16(AttnArgs a, AttnSplit s0,
-                                                                  AttnSplit s1, int n0) {
+                                                                  AttnSplit s1, unsigned n0,
+                                                                  unsigned first) {
     union Lds {
         TileLds<D> tile;
         StreamLds<D> stream;
         __device__ Lds() {}
     };
     __shared__ Lds lds;
-    if ((int)blockIdx.x < n0) tile_bf16<D>(a, s0, (int)blockIdx.x, lds.tile);
-    else stream_bf16<D, 2>(a, s1, (int)blockIdx.x - n0, lds.stream);
+    const unsigned block = first + blockIdx.x;
+    if (block < n0) tile_bf16<D>(a, s0, (int)block, lds.tile);
+    else stream_bf16<D, 2>(a, s1, (int)(block - n0), lds.stream);
 }
 
 // The lists of a call of many requests (AttnTable), a workgroup for each of
@@ -1211,15 +1216,27 @@ long far_keys(const AttnArgs& a) {
     return (long)(kFarBytes / key);
 }
 
+// Workgroups of a launch: a grid holds fewer than 2^32 threads, and the calls
+// that are accepted make up to 2^31 parts (one each for T Hq of 2^30).
+constexpr unsigned kGrid = 1u << 23;
+template <typename F>
+void in_grids(unsigned n, F launch) {
+    for (unsigned first = 0; first < n; first += kGrid) launch(n - first < kGrid ? n - first : kGrid, first);
+}
+
 template <int D>
 void launch_stream(const AttnArgs& a, const Plan& p, const Launch& l, hipStream_t st) {
-    const unsigned grid = (unsigned)l.items;
+    const auto run = [&](auto kernel) {
+        in_grids((unsigned)l.items, [&](unsigned grid, unsigned first) {
+            kernel<<<grid, kAttnThreads, 0, st>>>(a, l.split, first);
+        });
+    };
     if (a.bf16_io) {
-        if (p.RT == 1) attn_stream_bf16<D, 1><<<grid, kAttnThreads, 0, st>>>(a, l.split);
-        else attn_stream_bf16<D, 2><<<grid, kAttnThreads, 0, st>>>(a, l.split);
+        if (p.RT == 1) run(attn_stream_bf16<D, 1>);
+        else run(attn_stream_bf16<D, 2>);
     } else {
-        if (p.RT == 1) attn_stream_f32<D, 1><<<grid, kAttnThreads, 0, st>>>(a, l.split);
-        else attn_stream_f32<D, 2><<<grid, kAttnThreads, 0, st>>>(a, l.split);
+        if (p.RT == 1) run(attn_stream_f32<D, 1>);
+        else run(attn_stream_f32<D, 2>);
     }
 }
 
@@ -1228,11 +1245,15 @@ hipError_t launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
     const Launch &l0 = p.l[0], &l1 = p.l[p.n - 1];
     if (a.B > kBlock) attn_list<<<(unsigned)p.n, 64 * kListWaves, 0, st>>>(a, l0.split, l1.split);
     if constexpr (D >= 64) {
-        const unsigned n0 = (unsigned)l0.items, n = n0 + (unsigned)l1.items;
+        const unsigned n0 = (unsigned)l0.items;
         if (p.n == 2) {
-            attn_both_bf16<D><<<n, kAttnThreads, 0, st>>>(a, l0.split, l1.split, (int)n0);
+            in_grids(n0 + (unsigned)l1.items, [&](unsigned grid, unsigned first) {
+                attn_both_bf16<D><<<grid, kAttnThreads, 0, st>>>(a, l0.split, l1.split, n0, first);
+            });
         } else if (p.tiles) {
-            attn_tile_bf16<D><<<n0, kAttnThreads, 0, st>>>(a, l0.split);
+            in_grids(n0, [&](unsigned grid, unsigned first) {
+                attn_tile_bf16<D><<<grid, kAttnThreads, 0, st>>>(a, l0.split, first);
+            });
         }
     }
     if (!p.tiles) launch_stream<D>(a, p, l0, st);

@@ -273,19 +273,24 @@ template <typename T>
 void launch(const VerifyArgs& a, double* sums, hipStream_t st) {
     const int parts = parts_of(a.V);
     int* accs = (int*)(sums + (size_t)a.B * parts);
-    // at most 65535 requests a launch in the grid's second dimension
-    for (int b = 0; parts > 1 && b < a.B; b += 65535) {
+    // requests of a launch: at most 65535 in the grid's second dimension, and fewer
+    // than 2^32 threads in a grid
+    const long most = parts > 1 ? 65535 : 1 << 23;
+    for (long b = 0; b < a.B; b += most) {
+        const int n = (int)(a.B - b < most ? a.B - b : most);
         VerifyArgs c = a;
-        c.p = (const T*)a.p + (long)b * (a.T + 1) * a.V;
-        if (a.q) c.q = (const T*)a.q + (long)b * a.T * a.V;
-        c.x = a.x + (long)b * a.T;
-        c.u = a.u + (long)b * (a.T + 1);
+        c.p = (const T*)a.p + b * (a.T + 1) * a.V;
+        if (a.q) c.q = (const T*)a.q + b * a.T * a.V;
+        c.x = a.x + b * a.T;
+        c.u = a.u + b * (a.T + 1);
         if (a.n_draft) c.n_draft = a.n_draft + b;
-        const int n = a.B - b < 65535 ? a.B - b : 65535;
-        verify_sums<T><<<dim3((unsigned)parts, (unsigned)n), kThreads, 0, st>>>(
-            c, sums + (long)b * parts, accs + b);
+        c.n_commit = a.n_commit + b;
+        c.tokens = a.tokens + b * (a.T + 1);
+        if (parts > 1)
+            verify_sums<T><<<dim3((unsigned)parts, (unsigned)n), kThreads, 0, st>>>(
+                c, sums + b * parts, accs + b);
+        verify_pick<T><<<(unsigned)n, kThreads, 0, st>>>(c, sums + b * parts, accs + b, parts);
     }
-    verify_pick<T><<<(unsigned)a.B, kThreads, 0, st>>>(a, sums, accs, parts);
 }
 
 }  // namespace

@@ -55,10 +55,15 @@ hipError_t launch_cache_append(const void* k, const void* v, const int* slots, v
     const int row16 = row_bytes / 16;
     const long per_token = (long)Hkv * row16;
     const int tokens = per_token >= kPieces ? 1 : (int)(kPieces / per_token);
-    const unsigned grid = (unsigned)(((long)T + tokens - 1) / tokens);
+    // a grid holds fewer than 2^32 threads
+    const long most = ((long)1 << 23) * tokens;
     const auto run = [&](auto kernel) {
-        kernel<<<grid, kThreads, 0, st>>>((const u32x4*)k, (const u32x4*)v, slots, (u32x4*)kc,
-                                          (u32x4*)vc, T, Hkv, row16, page_shift, pool, tokens);
+        for (long t = 0; t < T; t += most) {
+            const int n = (int)(T - t < most ? T - t : most);
+            kernel<<<(unsigned)(((long)n + tokens - 1) / tokens), kThreads, 0, st>>>(
+                (const u32x4*)k + t * per_token, (const u32x4*)v + t * per_token, slots + t, (u32x4*)kc,
+                (u32x4*)vc, n, Hkv, row16, page_shift, pool, tokens);
+        }
     };
     if (4 * (size_t)T * Hkv * row_bytes > kStreamBytes) run(cache_append_kernel<true>);
     else run(cache_append_kernel<false>);

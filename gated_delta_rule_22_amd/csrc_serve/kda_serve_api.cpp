@@ -12,7 +12,8 @@
 namespace {
 
 constexpr size_t kMaxBytes = SIZE_MAX >> 3;
-constexpr size_t kMaxRows = (size_t)1 << 30;   // query rows, positions: 32-bit indices with room
+// query rows, positions, requests of a plan or an attention: 32-bit indices with room
+constexpr size_t kMaxRows = (size_t)1 << 30;
 
 bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 bool page_ok(int p) { return p >= 16 && p <= 1024 && (p & (p - 1)) == 0; }
@@ -60,7 +61,7 @@ kda_status done(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
 extern "C" {
 
 size_t kda_page_plan_workspace_size(int B) {
-    return B < 0 ? 0 : kda::page_plan_ws(B);
+    return B < 0 || (size_t)B > kMaxRows ? 0 : kda::page_plan_ws(B);
 }
 
 kda_status kda_page_plan(const int* kept_len, const int* n_new, const int* n_pages_in,
@@ -70,7 +71,7 @@ kda_status kda_page_plan(const int* kept_len, const int* n_new, const int* n_pag
                          int n_slots, void* ws, size_t ws_bytes, void* stream) {
     if (B < 0 || max_pages < 0 || n_pool < 0 || n_slots < 0) return KDA_ERR_INVALID_ARG;
     if (!page_ok(page_size)) return KDA_ERR_UNSUPPORTED;
-    if (!pool_ok(n_pool, page_size)) return KDA_ERR_INVALID_ARG;
+    if (!pool_ok(n_pool, page_size) || (size_t)B > kMaxRows) return KDA_ERR_INVALID_ARG;
     const size_t table = product(B, max_pages, 4);
     if (table > kMaxBytes) return KDA_ERR_INVALID_ARG;
     if (B && (!kept_len || !n_new || !n_pages_in || !n_pages_out)) return KDA_ERR_INVALID_ARG;
@@ -130,7 +131,8 @@ size_t kda_attn_paged_workspace_size(int T, int B, int Hq, int Hkv, int d, int m
                                      kda_dtype dtype) {
     if (T <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || !dim_ok(d) || max_new < 0) return 0;
     if (dtype != KDA_F32 && dtype != KDA_BF16) return 0;
-    if (product(T, Hq, d, 4) > kMaxBytes || product(T, Hq) > kMaxRows) return 0;
+    if (product(T, Hq, d, 4) > kMaxBytes || product(T, Hq) > kMaxRows || (size_t)B > kMaxRows)
+        return 0;
     return kda::attn_paged_ws(T, B, Hq, Hkv, d, max_new, dtype == KDA_BF16);
 }
 
@@ -151,7 +153,7 @@ kda_status kda_attn_paged(const void* q, const void* k_cache, const void* v_cach
     const size_t rows = product(T, Hq, d, elt), cache = product(n_pool, Hkv, page_size, d, elt);
     const size_t table = product(B, max_pages, 4);
     if (rows > kMaxBytes || cache > kMaxBytes || table > kMaxBytes ||
-        product(T, Hq) > kMaxRows || product(max_pages, page_size) > kMaxRows)
+        product(T, Hq) > kMaxRows || product(max_pages, page_size) > kMaxRows || (size_t)B > kMaxRows)
         return KDA_ERR_INVALID_ARG;
     if (!q || !o || !kept_len || !cu_new || (table && !block_table) ||
         (cache && (!k_cache || !v_cache)))

@@ -66,6 +66,7 @@ extern "C" {
  *               nothing is taken or given back (n_pages_out = n_pages_in,
  *               ring_out = ring_in), cu_new is 0 throughout and slot_map -1.
  *   page_size   a power of two, 16 .. 1024; n_pool * page_size <= INT32_MAX
+ *   B           at most 2^30
  *   ws          kda_page_plan_workspace_size() bytes
  * A call that is repeated with the same inputs (and other buffers for the
  * counts afterwards) gives the same outputs: what it writes to block_table
@@ -112,7 +113,7 @@ kda_status kda_cache_append(const void* k, const void* v, const int* slot_map,
  *   lse      [T, Hq] fp32 or NULL: natural log of the sum of exp(scores),
  *            -infinity for a row without any position
  *   scale    factor on q.k; 0 selects 1 / sqrt(d). Finite, not negative.
- *            T * Hq and max_pages * page_size are at most 2^30.
+ *            T * Hq, max_pages * page_size and B are at most 2^30.
  *   max_new  the largest number of new tokens of one request, 0 = unknown. It
  *            selects kernels only: results are right whatever it says.
  *   ws       kda_attn_paged_workspace_size() bytes

@@ -15,6 +15,8 @@ constexpr size_t kMaxBytes = SIZE_MAX >> 3;
 // query rows, positions, requests of a plan or an attention: 32-bit indices with room
 constexpr size_t kMaxRows = (size_t)1 << 30;
 
+constexpr float kMaxScale = 0x1p127f;          // scores are held times log2 e
+
 bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 bool page_ok(int p) { return p >= 16 && p <= 1024 && (p & (p - 1)) == 0; }
 bool pool_ok(int pool, int page) { return (long)pool * page <= INT32_MAX; }
@@ -143,7 +145,7 @@ kda_status kda_attn_paged(const void* q, const void* k_cache, const void* v_cach
                           kda_dtype dtype, void* ws, size_t ws_bytes, void* stream) {
     if (T < 0 || B < 0 || Hq < 0 || Hkv < 0 || n_pool < 0 || max_pages < 0 || max_new < 0)
         return KDA_ERR_INVALID_ARG;
-    if (!(scale >= 0.f) || isinf(scale)) return KDA_ERR_INVALID_ARG;
+    if (!(scale >= 0.f) || scale > kMaxScale) return KDA_ERR_INVALID_ARG;
     if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_UNSUPPORTED;
     if (!dim_ok(d) || !page_ok(page_size)) return KDA_ERR_UNSUPPORTED;
     if (!pool_ok(n_pool, page_size)) return KDA_ERR_INVALID_ARG;

@@ -112,7 +112,7 @@ kda_status kda_cache_append(const void* k, const void* v, const int* slot_map,
  *            gives 0.
  *   lse      [T, Hq] fp32 or NULL: natural log of the sum of exp(scores),
  *            -infinity for a row without any position
- *   scale    factor on q.k; 0 selects 1 / sqrt(d). Finite, not negative.
+ *   scale    factor on q.k; 0 selects 1 / sqrt(d). Not negative, at most 2^127.
  *            T * Hq, max_pages * page_size and B are at most 2^30.
  *   max_new  the largest number of new tokens of one request, 0 = unknown. It
  *            selects kernels only: results are right whatever it says.

@@ -25,3 +25,11 @@ def test_workspace_queries_refuse_them(B):
 def test_the_limit_itself_has_a_workspace():
     assert kda.kda_page_plan_workspace_size(MOST) > 0
     assert kda.kda_attn_paged_workspace_size(8, MOST, 8, 2, 64, 0, torch.bfloat16) > 0
+
+
+@no_gpu
+def test_scales_whose_product_with_log2_e_overflows_are_refused(lib):  # noqa: F811
+    for scale in (1.01 * 2.0 ** 127, 2.5e38, 3.4028234e38):
+        assert attn(lib, scale=scale) == INVALID, scale
+    for scale in (0.0, 1.0, 2.0 ** 127):
+        assert attn(lib, scale=scale) != INVALID, scale

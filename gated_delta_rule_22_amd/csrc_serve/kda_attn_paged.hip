@@ -1157,14 +1157,13 @@ struct Plan {
     Launch l[2];
     size_t bytes;          // workspace
 };
-Launch launch_of(long T, long B, long G, long Hkv, int R, int unit, int most_log2,
-                 int some_log2, int few_log2, int max_rows) {
+Launch launch_of(long T, long B, long G, long Hkv, int R, int most_log2, int some_log2,
+                 int few_log2, int max_rows) {
     Launch l{};
     l.split.R = R;
     l.split.R_log2 = __builtin_ctz((unsigned)R);
     l.split.min_rows = 1;
     l.split.max_rows = max_rows;
-    l.split.unit = unit;
     l.split.most_log2 = most_log2;
     l.split.some_log2 = some_log2;
     l.split.few_log2 = few_log2;
@@ -1185,12 +1184,12 @@ Plan plan_of(int T, int B, int Hq, int Hkv, int d, int max_new, bool bf16_io) {
     p.tiles = bf16_io && d >= 64 && most > kStreamRows;
     p.RT = most <= 16 ? 1 : 2;
     if (p.tiles) {
-        p.l[p.n] = launch_of(T, B, G, Hkv, kTileRows, 128, 9, 9, 9, INT32_MAX);
+        p.l[p.n] = launch_of(T, B, G, Hkv, kTileRows, 9, 9, 9, INT32_MAX);
         p.l[p.n].split.min_rows = kStreamRows + 1;
         ++p.n;
     }
     if (!p.tiles || B > 1) {
-        p.l[p.n] = launch_of(T, B, G, Hkv, 16 * p.RT, 128, 11, 10, 8, p.tiles ? kStreamRows : INT32_MAX);
+        p.l[p.n] = launch_of(T, B, G, Hkv, 16 * p.RT, 11, 10, 8, p.tiles ? kStreamRows : INT32_MAX);
         ++p.n;
     }
     // a single request is the tile kernel's whatever its length

@@ -33,13 +33,15 @@ constexpr int kLongPart = 1024;
 // sums instead of going through all requests: 1024 requests of one token over
 // 1000 positions 675 -> 4.6 + 640 us, 512 the same.
 constexpr int kBlock = 256;
+// Granularity and least length of a part: a step of the bf16 streams, two of
+// the other kernels.
+constexpr int kUnit = 128;
 
 // What a launch works on, besides AttnArgs.
 struct AttnSplit {
     int R, R_log2;      // rows of a tile, a power of two
     int min_rows;       // only requests of at least min_rows rows ...
     int max_rows;       // ... and at most max_rows of them
-    int unit;           // granularity and least length of a part, a power of two
     int most_log2;      // parts over the whole call: about as many as tiles, but not
     int some_log2;      // more than 2^most_log2, not fewer than 2^some_log2, and as few
     int few_log2;       // as 2^few_log2 rather than parts shorter than kLongPart
@@ -227,7 +229,7 @@ __device__ __forceinline__ int attn_part(const AttnArgs& a, const AttnSplit& s, 
     const float few = total * __builtin_bit_cast(float, (127 - s.few_log2) << 23);
     const float want = fmaxf(most, fminf(few, (float)kLongPart));
     // a part covers at most all positions
-    return __builtin_amdgcn_readfirstlane(((int)fminf(want, 1073741824.f) & ~(s.unit - 1)) + s.unit);
+    return __builtin_amdgcn_readfirstlane(((int)fminf(want, 1073741824.f) & ~(kUnit - 1)) + kUnit);
 }
 
 // The first wave's view of the call: one block of requests at a time, the only

@@ -295,7 +295,7 @@ void launch(const VerifyArgs& a, double* sums, hipStream_t st) {
 
 }  // namespace
 
-size_t draft_verify_ws(int B, int, int V) {
+size_t draft_verify_ws(int B, int V) {
     return parts_of(V) > 1 ? (size_t)B * (parts_of(V) * sizeof(double) + sizeof(int)) : 0;
 }
 

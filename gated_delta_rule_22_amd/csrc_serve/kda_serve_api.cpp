@@ -184,7 +184,7 @@ kda_status kda_attn_paged(const void* q, const void* k_cache, const void* v_cach
 }
 
 size_t kda_draft_verify_workspace_size(int B, int T, int V) {
-    return B <= 0 || T < 0 || V <= 0 ? 0 : kda::draft_verify_ws(B, T, V);
+    return B <= 0 || T < 0 || V <= 0 ? 0 : kda::draft_verify_ws(B, V);
 }
 
 kda_status kda_draft_verify(const void* target_probs, const void* draft_probs,

@@ -48,7 +48,7 @@ struct VerifyArgs {
     int B, T, V;
     bool bf16_io;
 };
-size_t draft_verify_ws(int B, int T, int V);
+size_t draft_verify_ws(int B, int V);
 hipError_t launch_draft_verify(const VerifyArgs& a, void* ws, hipStream_t st);
 
 }  // namespace kda

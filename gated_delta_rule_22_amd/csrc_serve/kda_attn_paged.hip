@@ -15,9 +15,13 @@
 // joined through LDS at the end. bf16, 32 query heads over 8 of 128: one token
 // of 256 requests over 1024 to 16384 positions (5.8 GB) 970 + 7 us, 6.0 TB/s;
 // 8 tokens of 4 over 65536 to 262144 (2.6 GB) 425 + 8 us, 6.2 TB/s; one token
-// over 1000 positions 8.4 + 4.3 us, all of it latency. fp32, 16 heads over 4:
-// 64 tokens over 4096 positions (1.1 GB) 200 us, 5.4 TB/s; 1024 tokens over
-// 1024 of width 64 83 us, half of the fp32 matrix rate.
+// over 1000 positions 8.2 + 4.5 us: memory latencies, and 2072
+// workgroups started of which 64 have a part. fp32, 16 heads over 4:
+// 64 tokens over 4096 positions (1.1 GB) 193 us, 5.6 TB/s; 1024 tokens over
+// 1024 of width 64 80 us, half of the fp32 matrix rate. Widths 32 and 16, bf16, 32
+// heads over 8: one token of 256 requests over 1024 to 8192 positions 172 and 94
+// us, 5.2 and 4.8 TB/s; 2048 tokens over 2048, in tiles of 32 rows that read the
+// keys again each, 102 and 98 us, where width 64 in tiles of 128 takes 109.
 #include "kda_attn_sched.h"
 
 #include <limits.h>
@@ -642,14 +646,13 @@ __device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, const voi
 //
 // As above S^T = K Q^T and O^T += V^T P^T, with the 32x32x16 product: the
 // scores of row l % 32 stay in lanes l and l + 32 and are the second operand
-// of the next product as they are. The scores of the next 64 keys are made
-// while the exponentials of these run, so that the matrix cores have work in
-// both; K is therefore fetched two steps ahead and V one, two buffers each.
+// of the next product as they are. K and V of the next 64 keys are fetched while
+// these are computed on, two buffers each and one barrier a step.
 //
 // 8192 tokens over 24576 positions, 32 heads over 8 of 128: 5.2 to 5.4 ms
-// from card to card, 5.8 TFLOP of products at 1.07 to 1.11 PFLOP/s; the clock
-// falls as the matrix cores fill, and a library product of 8192^3 reaches 1.20
-// PFLOP/s there. (Before the second terms: scores of the next 64 keys made while
+// from card to card, 5.8 TFLOP of products at 1.07 to 1.11 PFLOP/s with the matrix
+// cores busy 55% of the cycles at 1.9 GHz: the clock falls as they fill, and a
+// library product of 8192^3 reaches 1.20 PFLOP/s there. (Before the second terms: scores of the next 64 keys made while
 // the exponentials of these run, K fetched two steps ahead: the same at width
 // 128, 8% longer at 64, where the registers leave a workgroup less.)
 //
@@ -767,24 +770,24 @@ __device__ __forceinline__ void tile_bf16(const AttnArgs& a, const AttnSplit& s,
         }
     };
 
-    // One step: st holds the settled scores of the keys at pos (the step-th of
-    // the part), next receives those of the keys behind them.
-    int page_v = 0;                      // of K two steps ahead, V one
+    // One step: the 64 keys at pos, the step-th of the part.
+    int page_next = 0;                   // of this wave's 16 keys of the next step
     auto advance = [&](int pos, int step) {
         const int buf = step & 1;
         const bf16* kt = kbuf + buf * kTile;
         f32x16 st[2];
         bf16* vt = vbuf + buf * kTile;
-        // pages missing in the keys two steps ahead: known to the wave that
-        // fetches them. Four sets of flags: a wave sets those of one step while
-        // another still reads an older one's.
-        if (lane == 0) gap_wave[(step + 1) & 3][wave] = page_v < 0;
+        // pages missing in the next step's keys: known to the wave that fetches
+        // them. Three sets of flags are in use before the barrier: the next step's
+        // are set, this step's are, and a slower wave still reads the last one's.
+        // (Four, for the mask.)
+        if (lane == 0) gap_wave[(step + 1) & 3][wave] = page_next < 0;
         __builtin_amdgcn_s_waitcnt(0x0f70);          // vmcnt(0): this wave's part has landed
         __syncthreads();
         const bool more = pos + 64 < keys.end;
-        if (more) fetch(a.kc, kbuf + (buf ^ 1) * kTile, koff, pos + 64, page_v);
-        if (more) fetch(a.vc, vbuf + (buf ^ 1) * kTile, voff, pos + 64, page_v);
-        page_v = page_of(pos + 128);
+        if (more) fetch(a.kc, kbuf + (buf ^ 1) * kTile, koff, pos + 64, page_next);
+        if (more) fetch(a.vc, vbuf + (buf ^ 1) * kTile, voff, pos + 64, page_next);
+        page_next = page_of(pos + 128);
         bool odd = false;
         const int missing = missing_of(step);
         if (pos + 64 > keys.all || missing) {
@@ -858,7 +861,7 @@ __device__ __forceinline__ void tile_bf16(const AttnArgs& a, const AttnSplit& s,
 
     if (keys.begin < keys.end) {
         const int p0 = page_of(keys.begin);
-        page_v = page_of(keys.begin + 64);
+        page_next = page_of(keys.begin + 64);
         if (lane == 0) gap_wave[0][wave] = p0 < 0;
         fetch(a.kc, kbuf, koff, keys.begin, p0);
         fetch(a.vc, vbuf, voff, keys.begin, p0);
@@ -1137,13 +1140,13 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs a, AttnSplit 
 //
 // Up to kStreamRows rows a request is the stream kernels'; of a call with
 // larger ones (bf16, d of 64 and 128) those are the tile kernel's. At 64: 64
-// requests of 64 rows over 4000 positions 187 -> 291 us, 16 over 2000 42 -> 36
-// us. Parts: see AttnSplit. Streams, at most 2048 and at least 1024 of them
-// (4 long contexts: 480 us with 2048, 425 with 1024), 256 short ones (with 512:
-// 31 + 13 us in a ragged fp32 batch instead of 28 + 5). Tiles, 512, what the
-// card holds at once (256: 512 tokens over 3000 positions 53 instead of 44 us,
-// 1024: 52), of 128 keys or more (64: 528 tokens of 4 heads 16 instead of 13
-// us, 512: 17).
+// requests of 64 rows over 4000 positions 229 -> 247 us, 32 of 48 rows of width
+// 64 over 2000 77 -> 66. Parts: see AttnSplit. Streams, at most 2048 and at least
+// 1024 of them (4 long contexts: 480 us with 2048, 425 with 1024), 256 short ones
+// (with 512: 31 + 13 us in a ragged fp32 batch instead of 28 + 5). Tiles, 512,
+// what the card holds at once (256: 512 tokens over 3000 positions 66 instead of
+// 55 us, 1024: 65). Units of 128 keys (64: 528 tokens of 4 heads 15 instead of 12 us,
+// 512: 19).
 constexpr int kStreamRows = 32;
 
 struct Launch {
@@ -1172,8 +1175,9 @@ Launch launch_of(long T, long B, long G, long Hkv, int R, int most_log2, int som
     const long tiles = max_rows <= R ? (B < T ? B : T) * Hkv : attn_max_tiles(T, B, G, Hkv, R);
     l.items = attn_max_items(tiles, target);
     l.split.slots = (int)attn_max_slots(tiles, target);
-    // the joining's: a row or more each (2048 workgroups: 7 to 9 us more where
-    // there is little to join, no less where there is much)
+    // the joining's: a row or more each, at most 1024 for each of a call's splits
+    // (2048 for one: 7 to 9 us more where there is little to join, no less where
+    // there is much)
     const long rows = (tiles < target ? tiles : target) * R;
     l.joins = rows < 1024 ? rows : 1024;
     return l;

@@ -31,7 +31,7 @@ constexpr int kLongPart = 1024;
 // Requests that a wave holds, four a lane. With more of them a launch of its
 // own (attn_list) sums the blocks of this many once, and a workgroup reads the
 // sums instead of going through all requests: 1024 requests of one token over
-// 1000 positions 675 -> 4.6 + 640 us, 512 the same.
+// 1000 positions 675 -> 4.8 + 643 us.
 constexpr int kBlock = 256;
 // Granularity and least length of a part: a step of the bf16 streams, two of
 // the other kernels.
@@ -145,8 +145,10 @@ struct AttnBlock {
         return (long)r0.tiles * r0.kv + (long)r1.tiles * r1.kv +
                ((long)r2.tiles * r2.kv + (long)r3.tiles * r3.kv);
     }
-    // ceil(kv / C) in fp32: C is a multiple of 64, so the quotient is off by
-    // less than 2^-24 * 2^24 / 64 and one comparison mends it
+    // ceil(kv / C) in fp32. C is above the call's work over 2^most_log2, and kv is
+    // part of that work: the quotient is below 2^11, the three roundings in it move
+    // it by far less than 1, and a comparison to either side mends it. (A request
+    // without tiles has no part in the work, and its parts count for nothing.)
     static __device__ int parts(int kv, int C, float rC) {
         int n = (int)((float)kv * rC);
         n = max(n, 1);

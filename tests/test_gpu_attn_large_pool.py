@@ -61,3 +61,47 @@ def test_much_and_little_of_a_pool(pool, n, hint, copies):
 def test_hint_too_small(pool):
     # rows of a request in several tiles of the streams, which read its keys again
     run(pool, [70, 1, 33, 2], [2100, 1999, 2300, 2150], 2, 60, 1)
+
+
+@pytest.mark.parametrize("n", [1, 12])
+def test_replays_with_lengths_of_both_kinds(pool, n):
+    # one captured call of more than a block of requests, replayed with lengths that
+    # read little and much; each replay gives what the eager call gives
+    kc, vc = pool
+    d, B = kc.shape[3], 300
+    small = R.attn_case([n] * 3, [2500] * 3, 2 * HKV, HKV, d, PAGE, BF, seed=5 + n)
+    used = small["kc"].shape[0]
+    kc[POOL - used:], vc[POOL - used:] = small["kc"].to(DEV), small["vc"].to(DEV)
+    table = torch.where((small["table"] >= 0) & (small["table"] < used),
+                        small["table"] + POOL - used, small["table"]).to(DEV).repeat(B // 3, 1)
+    q = small["q"].to(DEV).repeat(B // 3, 1, 1)
+    cu = ints([n * i for i in range(B + 1)])
+    kept = ints([2500] * B)
+    o, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device=DEV)
+    ws = torch.empty(kda.kda_attn_paged_workspace_size(q.shape[0], B, 2 * HKV, HKV, d, n, BF),
+                     dtype=torch.uint8, device=DEV)
+
+    def step():
+        kda.kda_attn_paged(q, kc, vc, table, kept, cu, o=o, lse=lse, max_new=n, workspace=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for length in (2500, 100, 2400, 30, 2500):
+        kept.fill_(length)
+        o.zero_()
+        step()
+        torch.cuda.synchronize()
+        ro, rl = o.clone(), lse.clone()
+        o.zero_()
+        ws.fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, ro) and torch.equal(lse, rl), length
+        c = dict(small, kept=[length] * 3)
+        verdict(c, o[:3 * n].cpu(), lse[:3 * n].cpu(), R.attn(c))

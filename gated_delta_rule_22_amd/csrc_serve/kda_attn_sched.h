@@ -67,7 +67,8 @@ struct AttnItem {
 struct AttnReq { int n, kv, tiles, row0, kept; bool back; };
 
 // A request from its offsets and length as they are stored; in = false: none.
-__device__ __forceinline__ AttnReq attn_req(const AttnArgs& a, const AttnSplit& s, bool in, int lo,
+template <typename A>
+__device__ __forceinline__ AttnReq attn_req(const A& a, const AttnSplit& s, bool in, int lo,
                                             int hi, int kept) {
     AttnReq r;
     lo = min(max(lo, 0), a.T);
@@ -76,8 +77,9 @@ __device__ __forceinline__ AttnReq attn_req(const AttnArgs& a, const AttnSplit& 
     r.row0 = lo;
     r.n = in ? max(hi - lo, 0) : 0;
     r.back = in && hi < lo;
-    r.kept = min(max(kept, 0), cap);
+    r.kept = min(max(kept, A::kLeastKept), cap);
     r.kv = r.kept + min(r.n, cap - r.kept);
+    if constexpr (A::kLeastKept < 0) r.kv = max(r.kv, 0);
     const int rows = r.n * (a.Hq / a.Hkv);           // at most T Hq
     r.tiles = rows >= s.min_rows && rows <= s.max_rows ? (rows + s.R - 1) >> s.R_log2 : 0;
     return r;
@@ -123,13 +125,14 @@ struct AttnBlock {
     int f1, f2, f3, mine, p; // items before the 2nd .. 4th request, in all, and the prefix
     int c1, c2, c3, cut, q;  // the same for partial results
 
-    __device__ void load(const AttnArgs& a, const AttnSplit& s, int base) {
-        // no branch between the loads: one memory latency for all nine
+    template <typename A>
+    __device__ void load(const A& a, const AttnSplit& s, int base) {
+        // no branch between the loads: one memory latency for all of them
         const int i = base + 4 * (threadIdx.x & 63), last = a.B - 1;
         const int u0 = a.cu[min(i, a.B)], u1 = a.cu[min(i + 1, a.B)], u2 = a.cu[min(i + 2, a.B)],
                   u3 = a.cu[min(i + 3, a.B)], u4 = a.cu[min(i + 4, a.B)];
-        const int k0 = a.kept[min(i, last)], k1 = a.kept[min(i + 1, last)],
-                  k2 = a.kept[min(i + 2, last)], k3 = a.kept[min(i + 3, last)];
+        const int k0 = a.kept_of(min(i, last)), k1 = a.kept_of(min(i + 1, last)),
+                  k2 = a.kept_of(min(i + 2, last)), k3 = a.kept_of(min(i + 3, last));
         r0 = attn_req(a, s, i <= last, u0, u1, k0);
         r1 = attn_req(a, s, i + 1 <= last, u1, u2, k1);
         r2 = attn_req(a, s, i + 2 <= last, u2, u3, k2);
@@ -242,7 +245,8 @@ struct AttnSched {
     int C, items;
     bool far;
 
-    __device__ void init(const AttnArgs& a, const AttnSplit& s) {
+    template <typename A>
+    __device__ void init(const A& a, const AttnSplit& s) {
         if (s.table) {
             C = __builtin_amdgcn_readfirstlane(s.table[0]);
             items = __builtin_amdgcn_readfirstlane(s.table[UNITS ? 2 : 1]);
@@ -258,7 +262,8 @@ struct AttnSched {
         if (__any(block.back()) && wave_total(block.claims()) > a.T) items = 0;
     }
     // The y-th item of the call into LDS; found = false behind the last.
-    __device__ void find(const AttnArgs& a, const AttnSplit& s, int y, AttnItem* to) {
+    template <typename A>
+    __device__ void find(const A& a, const AttnSplit& s, int y, AttnItem* to) {
         if (threadIdx.x == 0) to->found = false;
         if (y >= items) return;
         int base = 0, before = 0, slot0 = 0;
@@ -306,7 +311,8 @@ __device__ __forceinline__ AttnItem attn_shared(const AttnItem& lds) {
 }
 
 // The x-th part of the call.
-__device__ __forceinline__ AttnItem attn_item(const AttnArgs& a, const AttnSplit& s, int x,
+template <typename A>
+__device__ __forceinline__ AttnItem attn_item(const A& a, const AttnSplit& s, int x,
                                               AttnItem& lds) {
     if (wave_id() == 0) {
         AttnSched<false> sched;

@@ -35,6 +35,8 @@ struct AttnArgs {
     int max_new;          // a hint, 0 = unknown
     float scale;
     bool bf16_io;
+    static constexpr int kLeastKept = 0;
+    __device__ int kept_of(int i) const { return kept[i]; }
 };
 size_t attn_paged_ws(int T, int B, int Hq, int Hkv, int d, int max_new, bool bf16_io);
 hipError_t launch_attn_paged(const AttnArgs& a, void* ws, hipStream_t st);

@@ -25,6 +25,9 @@ __all__ = [
     "kda_page_plan_workspace_size", "kda_page_plan", "kda_cache_append",
     "kda_attn_paged_workspace_size", "kda_attn_paged", "kda_draft_verify_workspace_size",
     "kda_draft_verify", "KDA_PLAN_OK", "KDA_PLAN_INVALID", "KDA_PLAN_NO_SLOTS",
+    "KDARope", "kda_rope_freqs", "kda_rope_append", "kda_latent_append",
+    "kda_attn_latent_workspace_size", "kda_attn_latent", "kda_attn_expanded_workspace_size",
+    "kda_attn_expanded",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -90,6 +93,7 @@ def load_library():
                                             vp]
     lib.kda_prefill_fwd_noalloc.restype = i
     serve.declare(lib)
+    full.declare(lib)
     _lib = lib
     return lib
 
@@ -466,3 +470,7 @@ from .serve import (  # noqa: E402
     KDA_PLAN_INVALID, KDA_PLAN_NO_SLOTS, KDA_PLAN_OK, kda_attn_paged,
     kda_attn_paged_workspace_size, kda_cache_append, kda_draft_verify,
     kda_draft_verify_workspace_size, kda_page_plan, kda_page_plan_workspace_size)
+from . import full  # noqa: E402
+from .full import (  # noqa: E402
+    KDARope, kda_attn_expanded, kda_attn_expanded_workspace_size, kda_attn_latent,
+    kda_attn_latent_workspace_size, kda_latent_append, kda_rope_append, kda_rope_freqs)

@@ -23,7 +23,9 @@ FLAGS = [
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_prefill_generic.hip", "kda_prefill_mfma.hip",
            "kda_varlen.hip", "kda_epilogue.hip", "kda_decode_multi_mfma.hip",
            "kda_serve_api.cpp", "kda_page_plan.hip", "kda_cache_append.hip",
-           "kda_attn_paged.hip", "kda_draft_verify.hip"]
+           "kda_attn_paged.hip", "kda_draft_verify.hip",
+           "kda_full_api.cpp", "kda_rope_append.hip", "kda_latent_append.hip",
+           "kda_attn_latent.hip", "kda_attn_expanded.hip"]
 
 
 def _path(src: str) -> str:

@@ -1,0 +1,261 @@
+"""C ABI of the full-attention layers without a GPU: declared symbols are exported,
+every bad argument is rejected on the host before any launch, and the rotation's
+frequencies are what they are said to be."""
+import ctypes
+import math
+import os
+import re
+
+import pytest
+import torch
+
+import gated_delta_rule_22_amd as kda
+from gated_delta_rule_22_amd.full import _RopeStruct
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+I31 = 2**31 - 1
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(kda.lib_path()):
+        import __graft_entry__
+        __graft_entry__.build()
+    return kda.load_library()
+
+
+# made-up, well spaced device addresses: only where no GPU is visible, so that a call
+# that wrongly passes the checks fails to launch instead of touching them
+BASE = 1 << 40
+no_gpu = pytest.mark.skipif(os.path.exists("/dev/kfd"),
+                            reason="fake device addresses: run only where no GPU is visible")
+
+
+def P(i, off=0):
+    return ctypes.c_void_p(BASE + (i << 38) + off)
+
+
+def rope(freqs=P(20), rot=64, interleaved=0, factor=1.0):
+    return _RopeStruct(freqs, rot, interleaved, factor)
+
+
+def test_exports_every_declared_symbol(lib):
+    text = open(os.path.join(ROOT, "include", "kda_full.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    syms = set(re.findall(r"\b(kda_[a-z0-9_]+)\s*\(", text))
+    assert syms == {"kda_rope_append", "kda_latent_append", "kda_attn_latent_workspace_size",
+                    "kda_attn_latent", "kda_attn_expanded_workspace_size", "kda_attn_expanded"}
+    for s in syms:
+        assert hasattr(lib, s) and s in kda.__all__, s
+
+
+def rope_append(lib, **kw):
+    a = dict(q=P(0), k=P(1), v=P(2), slot=P(3), kept=P(4), cu=P(5), qo=P(6), kc=P(7), vc=P(8), T=8, B=4,
+             Hq=4, Hkv=2, d=64, page=64, pool=10, rope=rope(), dt=1)
+    a.update(kw)
+    r = a["rope"]
+    return lib.kda_rope_append(*[a[k] for k in ("q", "k", "v", "slot", "kept", "cu", "qo", "kc", "vc", "T",
+                                                "B", "Hq", "Hkv", "d", "page", "pool")],
+                               None if r is None else ctypes.byref(r), a["dt"], None)
+
+
+@no_gpu
+def test_rope_append_rejects(lib):
+    for name in ("T", "B", "Hq", "Hkv", "pool"):
+        assert rope_append(lib, **{name: -1}) == INVALID, name
+    for name in ("T", "B"):
+        assert rope_append(lib, **{name: 0}) == OK, name
+    assert rope_append(lib, Hq=0, Hkv=0) == OK
+    for kw in (dict(d=48), dict(d=256), dict(page=24), dict(dt=5)):
+        assert rope_append(lib, **kw) == UNSUPPORTED, kw
+    for name in ("q", "k", "v", "qo", "kc", "vc"):
+        assert rope_append(lib, **{name: None}) == INVALID, name
+        assert rope_append(lib, **{name: P(9, 8)}) == INVALID, name
+    for name in ("slot", "kept", "cu"):
+        assert rope_append(lib, **{name: None}) == INVALID, name
+        assert rope_append(lib, **{name: P(9, 2)}) == INVALID, name
+    for r in (None, rope(freqs=None), rope(freqs=P(20, 4)), rope(rot=0), rope(rot=-16), rope(rot=24),
+              rope(rot=80), rope(factor=math.nan), rope(factor=math.inf)):
+        assert rope_append(lib, rope=r) == INVALID
+    assert rope_append(lib, qo=P(0, 64)) == INVALID              # partly over q
+    assert rope_append(lib, kc=P(1)) == INVALID
+    assert rope_append(lib, vc=P(7, 1024)) == INVALID
+    assert rope_append(lib, qo=P(20)) == INVALID                 # over the frequencies
+    assert rope_append(lib, kc=P(3)) == INVALID
+    assert rope_append(lib, pool=1 << 25) == INVALID
+    assert rope_append(lib, T=I31) == INVALID
+    assert rope_append(lib, T=I31, Hq=I31, Hkv=I31) == INVALID
+    assert rope_append(lib, T=1, Hq=0, Hkv=1 << 30, pool=0) == INVALID
+
+
+def latent_append(lib, **kw):
+    a = dict(kv=P(0), w=P(1), slot=P(2), kept=P(3), cu=P(4), cache=P(5), kvo=P(6), q=P(7), qo=P(8), T=8, B=4,
+             Hq=4, dq=192, dqo=576, dc=512, dr=64, page=64, pool=10, norm=1, eps=1e-6, rope=rope(), dt=1)
+    a.update(kw)
+    r = a["rope"]
+    return lib.kda_latent_append(*[a[k] for k in ("kv", "w", "slot", "kept", "cu", "cache", "kvo", "q", "qo",
+                                                  "T", "B", "Hq", "dq", "dqo", "dc", "dr", "page", "pool",
+                                                  "norm", "eps")],
+                                 None if r is None else ctypes.byref(r), a["dt"], None)
+
+
+@no_gpu
+def test_latent_append_rejects(lib):
+    for name in ("T", "B", "Hq", "pool"):
+        assert latent_append(lib, **{name: -1}) == INVALID, name
+    for name in ("T", "B"):
+        assert latent_append(lib, **{name: 0}) == OK, name
+    for kw in (dict(dc=64), dict(dc=576), dict(dr=32), dict(dr=0), dict(page=8), dict(dt=2)):
+        assert latent_append(lib, **kw) == UNSUPPORTED, kw
+    for name in ("kv", "slot", "kept", "cu", "cache", "q", "qo"):
+        assert latent_append(lib, **{name: None}) == INVALID, name
+    for name in ("kv", "w", "cache", "kvo", "q", "qo"):
+        assert latent_append(lib, **{name: P(9, 8)}) == INVALID, name
+    for name in ("slot", "kept", "cu"):
+        assert latent_append(lib, **{name: P(9, 2)}) == INVALID, name
+    for kw in (dict(dq=56), dict(dqo=60), dict(dq=196), dict(dqo=-64), dict(eps=-1e-6), dict(eps=math.nan),
+               dict(eps=math.inf), dict(norm=0), dict(rope=rope(rot=32)), dict(rope=rope(freqs=None))):
+        assert latent_append(lib, **kw) == INVALID, kw
+    assert latent_append(lib, kvo=P(0, 1152)) == INVALID         # partly over kv
+    assert latent_append(lib, qo=P(7)) == INVALID                # in place, but wider
+    assert latent_append(lib, qo=P(7, 64), dqo=192) == INVALID
+    assert latent_append(lib, cache=P(6)) == INVALID
+    assert latent_append(lib, cache=P(0)) == INVALID
+    assert latent_append(lib, qo=P(1)) == INVALID
+    assert latent_append(lib, pool=1 << 25) == INVALID
+    assert latent_append(lib, T=I31) == INVALID
+    assert latent_append(lib, T=I31, Hq=I31, dq=2**30, dqo=2**30) == INVALID
+
+
+def attn_latent(lib, **kw):
+    a = dict(q=P(0), cache=P(1), table=P(2), kept=P(3), cu=P(4), o=P(5), lse=P(6), T=40, B=4, Hq=8, dc=512,
+             dr=64, page=64, pool=100, width=16, max_new=0, scale=0.1, dt=1, ws=P(7), wsz=1 << 34)
+    a.update(kw)
+    return lib.kda_attn_latent(*[a[k] for k in ("q", "cache", "table", "kept", "cu", "o", "lse", "T", "B", "Hq",
+                                                "dc", "dr", "page", "pool", "width", "max_new", "scale", "dt",
+                                                "ws", "wsz")], None)
+
+
+@no_gpu
+def test_attn_latent_rejects(lib):
+    for name in ("T", "B", "Hq", "pool", "width", "max_new"):
+        assert attn_latent(lib, **{name: -1}) == INVALID, name
+    for name in ("T", "B", "Hq"):
+        assert attn_latent(lib, **{name: 0}) == OK, name
+    for kw in (dict(dc=96), dict(dr=32), dict(page=8), dict(dt=2)):
+        assert attn_latent(lib, **kw) == UNSUPPORTED, kw
+    for s in (0.0, -1.0, math.nan, math.inf, 3e38):
+        assert attn_latent(lib, scale=s) == INVALID, s
+    for name in ("q", "cache", "table", "kept", "cu", "o"):
+        assert attn_latent(lib, **{name: None}) == INVALID, name
+    for name in ("q", "cache", "o"):
+        assert attn_latent(lib, **{name: P(9, 8)}) == INVALID, name
+    for name in ("table", "kept", "cu", "lse"):
+        assert attn_latent(lib, **{name: P(9, 2)}) == INVALID, name
+    need = kda.kda_attn_latent_workspace_size(40, 4, 8, 512, 64, 0, BF)
+    assert need > 0
+    assert attn_latent(lib, ws=None) == WORKSPACE
+    assert attn_latent(lib, wsz=need - 1) == WORKSPACE
+    assert attn_latent(lib, ws=P(7, 8)) == INVALID
+    assert attn_latent(lib, ws=P(1, 256)) == INVALID
+    assert attn_latent(lib, o=P(0)) == INVALID
+    assert attn_latent(lib, o=P(1, 4096)) == INVALID
+    assert attn_latent(lib, lse=P(5, 16)) == INVALID
+    assert attn_latent(lib, T=I31) == INVALID
+    assert attn_latent(lib, B=I31) == INVALID
+    assert attn_latent(lib, width=1 << 26) == INVALID
+
+
+def attn_expanded(lib, **kw):
+    a = dict(q=P(0), kv=P(1), pe=P(2), cq=P(3), ck=P(4), o=P(5), lse=P(6), T=40, N=90, B=4, H=8, dn=128, dr=64,
+             dv=128, ld=576, max_q=0, scale=0.0, dt=1, ws=P(7), wsz=1 << 34)
+    a.update(kw)
+    return lib.kda_attn_expanded(*[a[k] for k in ("q", "kv", "pe", "cq", "ck", "o", "lse", "T", "N", "B", "H",
+                                                  "dn", "dr", "dv", "ld", "max_q", "scale", "dt", "ws", "wsz")],
+                                 None)
+
+
+@no_gpu
+def test_attn_expanded_rejects(lib):
+    for name in ("T", "N", "B", "H", "max_q"):
+        assert attn_expanded(lib, **{name: -1}) == INVALID, name
+    for name in ("T", "B", "H"):
+        assert attn_expanded(lib, **{name: 0}) == OK, name
+    for kw in (dict(dn=96), dict(dn=64), dict(dv=64), dict(dr=32), dict(dt=2)):
+        assert attn_expanded(lib, **kw) == UNSUPPORTED, kw
+    for s in (-1.0, math.nan, math.inf):
+        assert attn_expanded(lib, scale=s) == INVALID, s
+    for ld in (56, 0, -64, 68):
+        assert attn_expanded(lib, ld=ld) == INVALID, ld
+    for name in ("q", "kv", "pe", "cq", "ck", "o"):
+        assert attn_expanded(lib, **{name: None}) == INVALID, name
+    for name in ("q", "kv", "pe", "o"):
+        assert attn_expanded(lib, **{name: P(9, 8)}) == INVALID, name
+    for name in ("cq", "ck", "lse"):
+        assert attn_expanded(lib, **{name: P(9, 2)}) == INVALID, name
+    need = kda.kda_attn_expanded_workspace_size(40, 4, 8, 128, 64, 128, 0, BF)
+    assert need > 0
+    assert attn_expanded(lib, ws=None) == WORKSPACE
+    assert attn_expanded(lib, wsz=need - 1) == WORKSPACE
+    assert attn_expanded(lib, ws=P(7, 8)) == INVALID
+    assert attn_expanded(lib, ws=P(0, 256)) == INVALID
+    assert attn_expanded(lib, o=P(0)) == INVALID
+    assert attn_expanded(lib, o=P(2, 90 * 576 * 2 - 1024 - 16)) == INVALID   # over the last row's end
+    assert attn_expanded(lib, lse=P(1)) == INVALID
+    assert attn_expanded(lib, T=I31) == INVALID
+    assert attn_expanded(lib, N=I31) == INVALID
+    assert attn_expanded(lib, B=I31) == INVALID
+
+
+def test_workspace_queries_refuse(lib):
+    for args in ((0, 1, 8, 512, 64, 0), (8, 0, 8, 512, 64, 0), (8, 1, 0, 512, 64, 0), (8, 1, 8, 500, 64, 0),
+                 (8, 1, 8, 512, 32, 0), (8, 1, 8, 512, 64, -1), (I31, 1, 8, 512, 64, 0),
+                 (8, I31, 8, 512, 64, 0)):
+        assert kda.kda_attn_latent_workspace_size(*args, BF) == 0, args
+    for args in ((0, 1, 8, 128, 64, 128, 0), (8, 0, 8, 128, 64, 128, 0), (8, 1, -1, 128, 64, 128, 0),
+                 (8, 1, 8, 128, 64, 64, 0), (8, 1, 8, 128, 0, 128, 0), (8, 1, 8, 128, 64, 128, -1),
+                 (I31, 1, 8, 128, 64, 128, 0), (8, I31, 8, 128, 64, 128, 0)):
+        assert kda.kda_attn_expanded_workspace_size(*args, BF) == 0, args
+
+
+def test_binding_refuses_host_tensors():
+    i = torch.zeros(4, dtype=torch.int32)
+    x, c = torch.zeros((4, 2, 64)), torch.zeros((3, 2, 16, 64))
+    with pytest.raises(ValueError, match="GPU"):
+        kda.KDARope(torch.zeros(32, dtype=torch.float64))
+    with pytest.raises(ValueError, match="GPU"):
+        kda.kda_rope_append(x, x, x, i, i, i, c, c, None)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.kda_latent_append(torch.zeros((4, 576)), i, i, i, torch.zeros((2, 16, 576)))
+    with pytest.raises(ValueError, match="GPU"):
+        kda.kda_attn_latent(torch.zeros((4, 2, 576)), torch.zeros((2, 16, 576)), i.view(4, 1), i, i, dc=512,
+                            scale=0.1)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.kda_attn_expanded(torch.zeros((4, 2, 192)), torch.zeros((4, 2, 256)), torch.zeros((4, 64)), i, i,
+                              dv=128)
+
+
+def test_rope_freqs():
+    f, factor = kda.kda_rope_freqs(8, base=10000.0)
+    assert factor == 1.0 and f.dtype == torch.float64
+    assert torch.allclose(f, torch.tensor([1.0, 0.1, 0.01, 0.001], dtype=torch.float64), rtol=1e-14)
+    g, factor = kda.kda_rope_freqs(8, scaling="linear", scale=4.0)
+    assert factor == 1.0 and torch.equal(g, f / 4)
+    g, factor = kda.kda_rope_freqs(8, scaling="base", scale=4.0)
+    assert factor == 1.0 and float(g[0]) == 1.0 and math.isclose(float(g[3]), 0.001 / 4, rel_tol=1e-12)
+    # over 1000 positions the pairs turn 159, 15.9, 1.59 and 0.159 times
+    g, factor = kda.kda_rope_freqs(8, scaling="parts", scale=16.0, original_len=1000)
+    assert math.isclose(factor, 0.1 * math.log(16.0) + 1.0, rel_tol=1e-15)
+    turns = 1000 / (2 * math.pi)
+    keep = [1.0, (turns * 0.1 - 1) / 31, (turns * 0.01 - 1) / 31, 0.0]
+    for j in range(4):
+        want = float(f[j]) * (keep[j] + (1 - keep[j]) / 16)
+        assert math.isclose(float(g[j]), want, rel_tol=1e-13), j
+    assert kda.kda_rope_freqs(8, scaling="parts", scale=1.0, original_len=1000)[1] == 1.0
+    for kw in (dict(rot=7), dict(rot=0), dict(rot=8, scaling="other"), dict(rot=8, scale=0.0),
+               dict(rot=8, base=-1.0), dict(rot=2, scaling="base"), dict(rot=8, scaling="parts"),
+               dict(rot=8, scaling="parts", original_len=10, fast=1.0, slow=2.0)):
+        with pytest.raises(ValueError):
+            kda.kda_rope_freqs(**kw)

@@ -12,7 +12,7 @@
 //           O^T += V^T P^T, so that V is read from LDS once, not by every wave.
 // The weights P pass through LDS in between, in the order of the second product's
 // operand.
-#include "kda_attn_rows.h"
+#include "kda_attn_even.h"
 #include "kda_full_launch.h"
 
 #include <limits.h>
@@ -34,6 +34,14 @@ __device__ __forceinline__ int latent_piece(int key, int c) {
     return c ^ (2 * (key >> 1 & 3) + (key >> 3 & 1));
 }
 
+// x as a value that is not known to be the same in every step: what is made from it
+// is made where it is used, not kept in registers that the rows' sums need. (Spilled
+// ones would be read back behind the loads in flight.)
+__device__ __forceinline__ int fresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // What a step needs of the request's pages: the 16 keys at pos + 16 u.
 template <int KT> struct StepPages {
     int id[KT / 16];
@@ -45,96 +53,128 @@ template <int KT> struct StepPages {
     }
 };
 
-template <int DC, int RT> struct LatentShape {
-    static constexpr int W = DC + kPe;
-    static constexpr int KG = 4 / RT;                // waves that share a row group
-    static constexpr int KT = RT == 1 ? 64 : 32;     // keys of a step
+// How eight waves share a tile of R rows: row groups of RTW row tiles of 16 (RGN),
+// key groups (KG) and, where a wave takes two row tiles, halves of the contraction
+// (HV): such a wave makes half the sums of both and adds the other half to one.
+template <int DC, int R_> struct LatentShape {
+    static constexpr int W = DC + kPe, R = R_, RP = R / 16;
+    static constexpr int KT = R == 32 ? 64 : 32;     // keys of a step
+    static constexpr int BUF = R == 32 ? 2 : 3;      // steps in LDS
+    static constexpr int HV = R == 128 ? 2 : 1, RTW = HV;
+    static constexpr int RGN = RP / RTW, KG = 8 / RGN / HV;
     static constexpr int NU = KT / 16 / KG;          // key tiles of a wave's scores
-    static constexpr int BUF = RT == 1 ? 2 : 3;      // steps in LDS
-    static constexpr int CT = DC / 64;               // value columns of a wave, in 16s
-    static constexpr int RP = 2 * RT;                // row tiles of 16
+    static constexpr int KS = W / 32 / HV;           // steps of their contraction
+    static constexpr int CT = DC / 128;              // value columns of a wave, in 16s
     static constexpr int KS2 = KT / 32;
-    static constexpr int kKeys = KT / 4;             // keys that a wave fetches
-    static constexpr int LD = kKeys * (W / 8) / 64;  // its loads
+    // Loads of 1 KB: of 16 keys, which one page holds, and the most of a wave. LW waves
+    // share 16 keys: wave x of them has the loads from load_of(x) on.
+    static constexpr int LW = 128 / KT, kLoads16 = 16 * (W / 8) / 64, LD = (kLoads16 + LW - 1) / LW;
+    static constexpr bool kUneven = kLoads16 % LW != 0;
+    __device__ static int load_of(int x) { return kLoads16 * x / LW; }
 };
+constexpr int kLatentThreads = 512;
 
-template <int DC, int RT> struct LatentLds {
-    typedef LatentShape<DC, RT> S;
+template <int DC, int R> struct LatentLds {
+    typedef LatentShape<DC, R> S;
     __align__(128) bf16 tile[S::BUF * S::KT * S::W];
     __align__(16) bf16 p[2 * S::RP * S::KS2 * 64 * 8];
-    float top[S::KG][32 * RT];
-    float factor[32 * RT], sum[S::KG][32 * RT];
-    int moved[4], odd[S::KT];
-    AttnItem item;
+    f32x4 half[S::HV > 1 ? 8 * S::NU * 64 : 1];
+    float top[S::KG][R], factor[R], sum[S::KG][R];
+    int moved[S::RP], odd[S::KT];
+    EvenItem item;
 };
 
-template <int DC, int RT>
-__global__ __launch_bounds__(kAttnThreads, 1) void attn_latent_bf16(AttnArgs a, AttnSplit s,
-                                                                    unsigned first_block) {
-    typedef LatentShape<DC, RT> S;
-    constexpr int W = S::W, KT = S::KT, NU = S::NU, BUF = S::BUF, CT = S::CT, LD = S::LD;
-    constexpr int KS = W / 32;                       // steps of the scores' contraction
-    constexpr int kPieces = W / 8;
-    __shared__ LatentLds<DC, RT> lds;
-    const AttnItem it = attn_item(a, s, (int)(first_block + blockIdx.x), lds.item);
-    if (!it.found) return;
+// One run: a piece of a tile's keys, or all of them.
+template <int DC, int R>
+__device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e, const EvenRun& it,
+                                           LatentLds<DC, R>& lds) {
+    typedef LatentShape<DC, R> S;
+    constexpr int W = S::W, KT = S::KT, NU = S::NU, BUF = S::BUF, CT = S::CT, LD = S::LD, RTW = S::RTW;
+    constexpr int KS = S::KS, kPieces = W / 8;
     const int wave = wave_id(), lane = threadIdx.x & 63;
     const int c16 = lane & 15, g4 = lane >> 4;
-    const int rg = wave % RT, kg = wave / RT;
-    const Keys keys = part_keys(a, s, it, a.Hq);
+    const int rg = wave % S::RGN, kg = S::HV > 1 ? 0 : wave / S::RGN, hv = S::HV > 1 ? wave / S::RGN : 0;
+    const Keys keys = run_keys(a, it, R);
     const_int* table = table_row(a, it.req);
     const float scale = a.scale * kLog2e;
     const int row_mask = (1 << a.page_shift) - 1;
+    const int row = (rg * RTW + hv) * 16 + c16;      // the lane's row of the tile
 
-    // queries of the wave's 32 rows
-    bf16x8 qf[2][KS];
-    int limit[2];                                    // last visible position
-    for (int rt = 0; rt < 2; ++rt) {
-        const RowAt x = row_at(a, it, a.Hq, it.tile * s.R + rg * 32 + rt * 16 + c16);
-        limit[rt] = x.in ? (int)min((long)it.kept + x.t, (long)kKeepAll) : -1;
-        const bf16* q = (const bf16*)a.q + x.q * W + 8 * g4;
-        for (int k = 0; k < KS; ++k) {
-            bf16x8 z = {};
-            if (x.in) z = *(const bf16x8*)(q + 32 * k);
-            qf[rt][k] = z;
-        }
+    bf16x8 qf[RTW][KS];
+#pragma unroll
+    for (int rt = 0; rt < RTW; ++rt) {
+        const RowAt x = run_row(a, it, it.tile * R + (rg * RTW + rt) * 16 + c16);
+        // (rows behind the request's read its first token's)
+        const bf16* q = (const bf16*)a.q + x.q * W + 32 * KS * hv + 8 * g4;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) qf[rt][k] = *(const bf16x8*)(q + 32 * k);
     }
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    const RowAt own = run_row(a, it, it.tile * R + row);
+    const int limit = own.in ? (int)min((long)it.kept + own.t, (long)kKeepAll) : -1;   // last visible position
+    float m = -INFINITY, l = 0.f;
     f32x4 acc[S::RP][CT];
+#pragma unroll
     for (int r = 0; r < S::RP; ++r)
+#pragma unroll
         for (int c = 0; c < CT; ++c) acc[r][c] = zero4();
 
-    // The lane's i-th 16 bytes of the wave's keys of a step: key fkey(i) of them,
-    // byte fcol(i) of its row.
-    auto fkey = [&](int i) { return (i * 64 + lane) / kPieces; };
-    auto fcol = [&](int i) {
-        const int x = i * 64 + lane, r = x / kPieces;
-        return 16 * latent_piece(wave * S::kKeys + r, x - r * kPieces);
+    // This wave's loads of a step: 16 keys (those at 16 u), some of their pieces of 16
+    // bytes in the order of LDS. Where in the keys' rows the lane's are is made anew in
+    // every step of the widest tiles, whose sums need the registers.
+    const int u = wave / S::LW, load0 = S::load_of(wave % S::LW);
+    const bool fewer = S::kUneven && S::load_of(wave % S::LW + 1) - load0 < LD;
+    const auto piece_at = [&](int i, int l, int& key, int& byte) {
+        const int x = (load0 + i) * 64 + l;
+        key = x / kPieces;
+        byte = 16 * latent_piece(key, x - key * kPieces);
     };
-    // A step's keys of this wave. Positions behind the end are read from the last
-    // one, which some row of the tile sees: nothing else of an unused row gets here.
-    auto fetch = [&](int buf, int pos, int page) {
-        const int base = pos + wave * S::kKeys;
-        bf16* to = lds.tile + (buf * KT + wave * S::kKeys) * W;
+    constexpr bool kKeep = R < 128;
+    uint32_t foff[kKeep ? LD : 1];
+    if (kKeep) {
+#pragma unroll
+        for (int i = 0; i < LD; ++i) {
+            int key, byte;
+            piece_at(i, lane, key, byte);
+            foff[i] = key * (2 * W) + byte;
+        }
+    }
+    // Positions behind the end are read from the last one, which some row of the tile
+    // sees: nothing else of an unused row gets here.
+    const auto fetch = [&](int buf, int pos, int page) {
+        bf16* to = lds.tile + (buf * KT + 16 * u) * W + load0 * 512;
         if (page >= 0) {
-            const int at = min(base, keys.end - 1);
+            const int at = uniform(min(pos + 16 * u, keys.end - 1)), most = keys.end - 1 - at;
             const bf16* from = (const bf16*)a.kc + (((long)page << a.page_shift) + (at & row_mask)) * W;
-            const int most = keys.end - 1 - at;
             const uint32_t l0 = uniform((int)(uint32_t)(uintptr_t)(lds_void*)to);
-            for (int i = 0; i < LD; ++i)
-                load_to_lds(l0 + i * 1024, min(fkey(i), most) * (2 * W) + fcol(i), from);
+            if (kKeep && most >= 15) {
+#pragma unroll
+                for (int i = 0; i < LD; ++i)
+                    if (i < LD - 1 || !fewer) load_to_lds(l0 + i * 1024, foff[i], from);
+            } else {
+                const int l = fresh(lane);
+#pragma unroll
+                for (int i = 0; i < LD; ++i) {
+                    if (i == LD - 1 && fewer) continue;
+                    int key, byte;
+                    piece_at(i, l, key, byte);
+                    load_to_lds(l0 + i * 1024, min(key, most) * (2 * W) + byte, from);
+                }
+            }
         } else {
-            for (int i = 0; i < LD; ++i) *(bf16x8*)(to + i * 512 + 8 * lane) = bf16x8{};
+            for (int i = 0; i < LD; ++i)
+                if (i < LD - 1 || !fewer) *(bf16x8*)(to + i * 512 + 8 * lane) = bf16x8{};
         }
     };
     const auto own_page = [&](const StepPages<KT>& p) {
         int x = p.id[0];
-        for (int u = 1; u < KT / 16; ++u) x = wave * S::kKeys / 16 == u ? p.id[u] : x;
+#pragma unroll
+        for (int i = 1; i < KT / 16; ++i) x = u == i ? p.id[i] : x;
         return uniform(x);
     };
     // Pages of 16 keys of which the first is behind the end: those of the last key.
     const auto pages_at = [&](int pos) {
         StepPages<KT> p;
+#pragma unroll
         for (int u = 0; u < KT / 16; ++u)
             p.id[u] = page_at(a, table, min(pos + 16 * u, keys.end - 1), keys.end);
         return p;
@@ -142,6 +182,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_latent_bf16(AttnArgs a, 
 
     StepPages<KT> pg[BUF];                           // of this step and those in flight
     if (keys.begin < keys.end) {
+#pragma unroll
         for (int b = 0; b < BUF - 1; ++b) {
             pg[b] = pages_at(keys.begin + b * KT);
             if (keys.begin + b * KT < keys.end) fetch(b, keys.begin + b * KT, own_page(pg[b]));
@@ -151,14 +192,18 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_latent_bf16(AttnArgs a, 
     int buf = 0;
     for (int pos = keys.begin; pos < keys.end; pos += KT) {
         // this wave's part of the step has landed; with three buffers the next
-        // step's loads may be in flight, if it has any
-        if (BUF == 3 && pos + KT < keys.end && own_page(pg[1]) >= 0) wait_loads<LD>();
-        else wait_loads<0>();
+        // step's loads may be in flight, if it has all of them
+        if (BUF == 3 && pos + KT < keys.end && own_page(pg[1]) >= 0) {
+            if (fewer) wait_loads<LD - 1>();
+            else wait_loads<LD>();
+        } else {
+            wait_loads<0>();
+        }
         __syncthreads();                             // everybody's, and the last step is done with
         const int last_buf = buf == 0 ? BUF - 1 : buf - 1;
-        if (pos + (BUF - 1) * KT < keys.end)
-            fetch(last_buf, pos + (BUF - 1) * KT, own_page(pg[BUF - 1]));
+        if (pos + (BUF - 1) * KT < keys.end) fetch(last_buf, pos + (BUF - 1) * KT, own_page(pg[BUF - 1]));
         const int missing = pg[0].missing();
+#pragma unroll
         for (int b = 0; b < BUF - 1; ++b) pg[b] = pg[b + 1];
         pg[BUF - 1] = pages_at(pos + BUF * KT);
         bf16* tile = lds.tile + buf * KT * W;
@@ -167,161 +212,186 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_latent_bf16(AttnArgs a, 
             // Positions that only some rows see: a value there that is not finite must
             // not meet the weight 0 of the others in a product. It counts 0, and the
             // scores of the rows that see its position become NaN.
-            bf16* x = tile + wave * S::kKeys * W;
-            if (lane < S::kKeys) lds.odd[wave * S::kKeys + lane] = 0;
-            lds_fence_wave();
+            if (threadIdx.x < KT) lds.odd[threadIdx.x] = 0;
+            __syncthreads();
             for (int i = 0; i < LD; ++i) {
-                if (fcol(i) >= 2 * DC) continue;
+                int key, byte;
+                piece_at(i, fresh(lane), key, byte);
+                if ((i == LD - 1 && fewer) || byte >= 2 * DC) continue;
                 bool odd = false;
-                bf16x8* v = (bf16x8*)(x + i * 512 + 8 * lane);
+                bf16x8* v = (bf16x8*)(tile + 16 * u * W + ((load0 + i) * 64 + lane) * 8);
                 *v = only_finite(*v, odd);
-                if (odd) lds.odd[wave * S::kKeys + fkey(i)] = 1;
+                if (odd) lds.odd[16 * u + key] = 1;
             }
             __syncthreads();
         }
 
-        // scores
-        f32x4 st[2][NU];
+        // scores: kAhead fragments of keys are in flight ahead of their products
+        f32x4 sc[RTW], st[NU];
+        constexpr int kAhead = KS < 6 ? KS : RTW > 1 ? 4 : 6;
+#pragma unroll
         for (int u = 0; u < NU; ++u) {
-            const bf16* k = tile + (16 * (kg * NU + u) + c16) * W;
-            st[0][u] = st[1][u] = zero4();
+            const bf16* from = tile + (16 * (kg * NU + u) + c16) * W;
+            // pieces first + 4 i + g4: the order of LDS repeats every eight
+            const int first = 4 * KS * hv;
+            const bf16* k[2] = {from + 8 * latent_piece(c16, first + g4), from + 8 * latent_piece(c16, first + 4 + g4)};
+            const auto read = [&](int i) { return *(const bf16x8*)(k[i & 1] + 64 * (i / 2)); };
+#pragma unroll
+            for (int rt = 0; rt < RTW; ++rt) sc[rt] = zero4();
+            bf16x8 kf[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) kf[i] = read(i);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
-                const bf16x8 kf = *(const bf16x8*)(k + 8 * latent_piece(c16, 4 * i + g4));
-                st[0][u] = mma32(kf, qf[0][i], st[0][u]);
-                st[1][u] = mma32(kf, qf[1][i], st[1][u]);
+#pragma unroll
+                for (int rt = 0; rt < RTW; ++rt) sc[rt] = mma32(kf[i % kAhead], qf[rt][i], sc[rt]);
+                if (i + kAhead < KS) kf[i % kAhead] = read(i + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            st[u] = sc[0];
+            if constexpr (S::HV > 1) {
+                // to the other half's wave its row tile's sums
+                lds.half[(wave * NU + u) * 64 + lane] = hv ? sc[0] : sc[1];
+                if (hv) st[u] = sc[1];
             }
         }
-        for (int rt = 0; rt < 2; ++rt)
-            for (int u = 0; u < NU; ++u)
-                for (int i = 0; i < 4; ++i) st[rt][u][i] *= scale;
+        if constexpr (S::HV > 1) {
+            lds_barrier();
+#pragma unroll
+            for (int u = 0; u < NU; ++u) st[u] += lds.half[((wave ^ 4) * NU + u) * 64 + lane];
+        }
+        for (int u = 0; u < NU; ++u)
+            for (int i = 0; i < 4; ++i) st[u][i] *= scale;
         if (pos + KT > keys.all || missing) {
             for (int u = 0; u < NU; ++u)
                 for (int i = 0; i < 4; ++i) {
                     const int y = 16 * (kg * NU + u) + 4 * g4 + i;
-                    const bool none = pos + y >= keys.end || (missing >> (kg * NU + u) & 1);
-                    const bool odd = partial && lds.odd[y];
-                    for (int rt = 0; rt < 2; ++rt) {
-                        if (odd) st[rt][u][i] = NAN;
-                        if (none || pos + y > limit[rt]) st[rt][u][i] = -INFINITY;
-                    }
+                    if (partial && lds.odd[y]) st[u][i] = NAN;
+                    if (pos + y >= keys.end || (missing >> (kg * NU + u) & 1) || pos + y > limit) st[u][i] = -INFINITY;
                 }
         }
-        float mx[2];
-        for (int rt = 0; rt < 2; ++rt) {
-            mx[rt] = -INFINITY;
-            for (int u = 0; u < NU; ++u)
-                for (int i = 0; i < 4; ++i) mx[rt] = fmaxf(mx[rt], st[rt][u][i]);
-            mx[rt] = max_quarters(mx[rt]);
-        }
+        float mx = -INFINITY;
+        for (int u = 0; u < NU; ++u)
+            for (int i = 0; i < 4; ++i) mx = fmaxf(mx, st[u][i]);
+        mx = max_quarters(mx);
         if constexpr (S::KG > 1) {
-            if (g4 == 0)
-                for (int rt = 0; rt < 2; ++rt) lds.top[kg][rg * 32 + rt * 16 + c16] = mx[rt];
-            __syncthreads();
-            for (int rt = 0; rt < 2; ++rt)
-                for (int k = 0; k < S::KG; ++k)
-                    mx[rt] = fmaxf(mx[rt], lds.top[k][rg * 32 + rt * 16 + c16]);
+            if (g4 == 0) lds.top[kg][row] = mx;
+            lds_barrier();
+            for (int k = 0; k < S::KG; ++k) mx = fmaxf(mx, lds.top[k][row]);
         }
         // The reference may stay behind the maximum by up to 8 in the log2 domain.
-        const bool moved = __any(mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f);
+        const bool moved = __any(mx > m + 8.f);
         if (moved) {
-            for (int rt = 0; rt < 2; ++rt) {
-                const float mn = fmaxf(m[rt], mx[rt]);
-                const float c = mn == -INFINITY ? 1.f : exp2_f(m[rt] - mn);
-                m[rt] = mn;
-                l[rt] *= c;
-                if (kg == 0 && g4 == 0) lds.factor[rg * 32 + rt * 16 + c16] = c;
-            }
+            const float mn = fmaxf(m, mx);
+            const float c = mn == -INFINITY ? 1.f : exp2_f(m - mn);
+            m = mn;
+            l *= c;
+            if (kg == 0 && g4 == 0) lds.factor[row] = c;
         }
-        if (kg == 0 && lane == 0) lds.moved[rg] = moved;
-        for (int rt = 0; rt < 2; ++rt) {
-            const float mu = m[rt] == -INFINITY ? 0.f : m[rt];
-            for (int u = 0; u < NU; ++u) {
-                float p[4];
-                for (int i = 0; i < 4; ++i) {
-                    p[i] = exp2_f(st[rt][u][i] - mu);
-                    l[rt] += p[i];
-                }
-                bf16x4 hi, lo;
-                two_terms(p, hi, lo);
-                const int t = kg * NU + u, r = rg * 2 + rt;
-                bf16* to = lds.p + ((r * S::KS2 + t / 2) * 64 + lane) * 8 + 4 * (t & 1);
-                *(bf16x4*)to = hi;
-                *(bf16x4*)(to + S::RP * S::KS2 * 512) = lo;
+        if (kg == 0 && lane == 0) lds.moved[rg * RTW + hv] = moved;
+        const float mu = m == -INFINITY ? 0.f : m;
+        for (int u = 0; u < NU; ++u) {
+            float p[4];
+            for (int i = 0; i < 4; ++i) {
+                p[i] = exp2_f(st[u][i] - mu);
+                l += p[i];
             }
+            bf16x4 hi, lo;
+            two_terms(p, hi, lo);
+            const int t = kg * NU + u, r = rg * RTW + hv;
+            bf16* to = lds.p + ((r * S::KS2 + t / 2) * 64 + lane) * 8 + 4 * (t & 1);
+            *(bf16x4*)to = hi;
+            *(bf16x4*)(to + S::RP * S::KS2 * 512) = lo;
         }
-        __syncthreads();
+        lds_barrier();
 
         // values
-        for (int g = 0; g < RT; ++g) {
-            if (!uniform(lds.moved[g])) continue;
-            for (int rt = 0; rt < 2; ++rt) {
-                const float c = lds.factor[g * 32 + rt * 16 + c16];
-                for (int b = 0; b < CT; ++b) acc[2 * g + rt][b] *= c;
+        int any_moved = 0;
+        for (int r = 0; r < S::RP; ++r) any_moved |= lds.moved[r];
+        if (uniform(any_moved)) {
+#pragma unroll
+            for (int r = 0; r < S::RP; ++r) {
+                const float c = lds.moved[r] ? lds.factor[r * 16 + c16] : 1.f;
+#pragma unroll
+                for (int b = 0; b < CT; ++b) acc[r][b] *= c;
             }
         }
 #pragma unroll
         for (int ks = 0; ks < S::KS2; ++ks) {
-            bf16x8 pf[S::RP], pr[S::RP];
-            for (int r = 0; r < S::RP; ++r) {
-                const bf16* x = lds.p + ((r * S::KS2 + ks) * 64 + lane) * 8;
-                pf[r] = *(const bf16x8*)x;
-                pr[r] = *(const bf16x8*)(x + S::RP * S::KS2 * 512);
-            }
-            const int key = 32 * ks + 4 * g4 + c16 / 4;
+            const int key = 4 * g4 + c16 / 4;        // (and 16 behind it: the same order in LDS)
+            bf16x8 va[CT];
 #pragma unroll
             for (int b = 0; b < CT; ++b) {
-                const int c = 2 * (wave * CT + b) + (c16 & 3) / 2;
-                const bf16* x = tile + key * W + 8 * latent_piece(key, c) + 4 * (c16 & 1);
+                // pieces of four b are in four orders, those behind them in the same
+                const int c = 2 * (wave * CT + b % 4) + (c16 & 3) / 2;
+                const bf16* x = tile + key * W + 8 * latent_piece(key, c) + 4 * (c16 & 1) + 64 * (b / 4) + 32 * ks * W;
                 const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)x);
                 const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(x + 16 * W));
-                const bf16x8 va = __builtin_bit_cast(
-                    bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-                for (int r = 0; r < S::RP; ++r) {
-                    acc[r][b] = mma32(va, pf[r], acc[r][b]);
-                    acc[r][b] = mma32(va, pr[r], acc[r][b]);
-                }
+                va[b] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            }
+#pragma unroll
+            for (int r = 0; r < S::RP; ++r) {
+                const bf16* x = lds.p + ((r * S::KS2 + ks) * 64 + lane) * 8;
+                const bf16x8 pf = *(const bf16x8*)x, pr = *(const bf16x8*)(x + S::RP * S::KS2 * 512);
+#pragma unroll
+                for (int b = 0; b < CT; ++b) acc[r][b] = mma32(va[b], pf, acc[r][b]);
+#pragma unroll
+                for (int b = 0; b < CT; ++b) acc[r][b] = mma32(va[b], pr, acc[r][b]);
             }
         }
         buf = buf + 1 == BUF ? 0 : buf + 1;
     }
 
     // the rows' sums and references, to all waves
-    for (int rt = 0; rt < 2; ++rt) {
-        const float sum = sum_quarters(l[rt]);
-        if (g4 == 0) {
-            lds.sum[kg][rg * 32 + rt * 16 + c16] = sum;
-            if (kg == 0) lds.top[0][rg * 32 + rt * 16 + c16] = m[rt];
-        }
+    const float part_sum = sum_quarters(l);
+    if (g4 == 0) {
+        lds.sum[kg][row] = part_sum;
+        if (kg == 0) lds.factor[row] = m;
     }
     __syncthreads();
-    for (int r = 0; r < S::RP; ++r) {
-        const int row = 16 * r + c16;
-        float sum = 0.f;
-        for (int k = 0; k < S::KG; ++k) sum += lds.sum[k][row];
-        const float top = lds.top[0][row];
-        const int col = wave * (DC / 4) + 4 * g4;
-        if (it.parts > 1) {
-            const long slot = (long)it.slot + (long)it.part * it.tiles + it.tile;
-            if ((unsigned long)slot >= (unsigned long)s.slots) return;   // (a guard)
-            const long at = slot * s.R + row;
-            // (a row without a key in this part has l = 0, and its values are not read)
-            for (int b = 0; sum != 0.f && b < CT; ++b)
-                *(f32x4*)(s.acc + at * DC + col + 16 * b) = acc[r][b];
-            if (wave == 0 && g4 == 0) { s.ml[at * 2] = top; s.ml[at * 2 + 1] = sum; }
-            continue;
+    const int col = wave * (16 * CT) + 4 * g4;
+    if (it.pieces > 1) {
+        float* to = e.acc + ((long)it.slot * R + c16) * DC + col;
+        // (a row without a key in this piece has l = 0, and its values are not used)
+#pragma unroll
+        for (int r = 0; r < S::RP; ++r)
+#pragma unroll
+            for (int b = 0; b < CT; ++b) *(f32x4*)(to + r * 16 * DC + 16 * b) = acc[r][b];
+        if (const int r = threadIdx.x; r < R) {
+            float sum = 0.f;
+            for (int k = 0; k < S::KG; ++k) sum += lds.sum[k][r];
+            e.ml[((long)it.slot * R + r) * 2] = lds.factor[r];
+            e.ml[((long)it.slot * R + r) * 2 + 1] = sum;
         }
-        const RowAt x = row_at(a, it, a.Hq, it.tile * s.R + row);
-        if (!x.in) continue;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        for (int b = 0; b < CT; ++b) {
-            bf16x4 y;
-            for (int i = 0; i < 4; ++i) y[i] = (bf16)(acc[r][b][i] * inv);
-            *(bf16x4*)((bf16*)a.o + x.q * DC + col + 16 * b) = y;
-        }
-        if (a.lse && wave == 0 && g4 == 0)
-            a.lse[x.q] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+        return;
     }
+#pragma unroll
+    for (int r = 0; r < S::RP; ++r) {
+        const int y = 16 * r + c16;
+        float sum = 0.f;
+        for (int k = 0; k < S::KG; ++k) sum += lds.sum[k][y];
+        const RowAt x = run_row(a, it, it.tile * R + y);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        bf16* to = (bf16*)a.o + x.q * DC + col;
+        if (x.in) {
+#pragma unroll
+            for (int b = 0; b < CT; ++b) {
+                bf16x4 z;
+                for (int i = 0; i < 4; ++i) z[i] = (bf16)(acc[r][b][i] * inv);
+                *(bf16x4*)(to + 16 * b) = z;
+            }
+            if (a.lse && wave == 0 && g4 == 0)
+                a.lse[x.q] = sum == 0.f ? -INFINITY : (lds.factor[y] + __log2f(sum)) * kLn2;
+        }
+    }
+}
+
+template <int DC, int R>
+__global__ __launch_bounds__(kLatentThreads, 2) void attn_latent_bf16(
+    AttnArgs a, AttnSplit s, EvenSplit e) {
+    __shared__ LatentLds<DC, R> lds;
+    even_runs(a, s, e, lds.item, [&](const EvenRun& it) { latent_run<DC, R>(a, e, it, lds); });
 }
 
 // fp32: 32 rows, 32 keys a step. Scores: a wave takes 16 rows and 16 keys, lane
@@ -334,29 +404,27 @@ template <int DC> struct LatentLdsF {
     __align__(16) float p[2 * 2 * 64 * 4];
     float top[2][32], factor[32], sum[2][32];
     int moved[2], odd[KT];
-    AttnItem item;
+    EvenItem item;
 };
+constexpr int kRowsF = 32;
 
 template <int DC>
-__global__ __launch_bounds__(kAttnThreads, 1) void attn_latent_f32(AttnArgs a, AttnSplit s,
-                                                                   unsigned first_block) {
+__device__ __forceinline__ void latent_run_f32(const AttnArgs& a, const EvenSplit& e, const EvenRun& it,
+                                               LatentLdsF<DC>& lds) {
     constexpr int W = DC + kPe, KT = 32, KQ = W / 16;   // pieces of a lane's channels
     constexpr int CT = DC / 64, VW = CT < 4 ? CT : 4;
     constexpr int kPieces = W / 4, kKeys = KT / 4, LD = kKeys * kPieces / 64;
-    __shared__ LatentLdsF<DC> lds;
-    const AttnItem it = attn_item(a, s, (int)(first_block + blockIdx.x), lds.item);
-    if (!it.found) return;
     const int wave = wave_id(), lane = threadIdx.x & 63;
     const int c16 = lane & 15, g4 = lane >> 4;
     const int rg = wave & 1, kg = wave >> 1;
-    const Keys keys = part_keys(a, s, it, a.Hq);
+    const Keys keys = run_keys(a, it, kRowsF);
     const_int* table = table_row(a, it.req);
     const float scale = a.scale * kLog2e;
     const int row_mask = (1 << a.page_shift) - 1;
     auto piece = [](int key, int c) { return c ^ (key & 15); };
 
     f32x4 qf[KQ];
-    const RowAt at_row = row_at(a, it, a.Hq, it.tile * s.R + rg * 16 + c16);
+    const RowAt at_row = run_row(a, it, it.tile * kRowsF + rg * 16 + c16);
     const int limit = at_row.in ? (int)min((long)it.kept + at_row.t, (long)kKeepAll) : -1;
     for (int k = 0; k < KQ; ++k) {
         f32x4 z = zero4();
@@ -490,60 +558,66 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_latent_f32(AttnArgs a, A
     for (int r = 0; r < 2; ++r) {
         const int row = 16 * r + c16;
         const float sum = lds.sum[0][row] + lds.sum[1][row], top = lds.top[0][row];
-        const bool cut = it.parts > 1;
-        const long slot = (long)it.slot + (long)it.part * it.tiles + it.tile;
-        if (cut && (unsigned long)slot >= (unsigned long)s.slots) return;   // (a guard)
-        const long at = slot * s.R + row;
-        const RowAt x = row_at(a, it, a.Hq, it.tile * s.R + row);
+        const bool cut = it.pieces > 1;
+        const long at = (long)it.slot * kRowsF + row;
+        const RowAt x = run_row(a, it, it.tile * kRowsF + row);
         if (!cut && !x.in) continue;
         const float inv = cut ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-        float* to = cut ? s.acc + at * DC : (float*)a.o + x.q * DC;
+        float* to = cut ? e.acc + at * DC : (float*)a.o + x.q * DC;
         for (int g = 0; (!cut || sum != 0.f) && g < CT / VW; ++g)
             for (int i = 0; i < 4; ++i)
                 for (int j = 0; j < VW; ++j)
                     to[wave * (DC / 4) + 16 * VW * g + VW * (4 * g4 + i) + j] = acc[r][g * VW + j][i] * inv;
         if (wave != 0 || g4 != 0) continue;
         if (cut) {
-            s.ml[at * 2] = top;
-            s.ml[at * 2 + 1] = sum;
+            e.ml[at * 2] = top;
+            e.ml[at * 2 + 1] = sum;
         } else if (a.lse) {
             a.lse[x.q] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
         }
     }
 }
 
+template <int DC>
+__global__ __launch_bounds__(kAttnThreads, 1) void attn_latent_f32(AttnArgs a, AttnSplit s, EvenSplit e) {
+    __shared__ LatentLdsF<DC> lds;
+    even_runs(a, s, e, lds.item, [&](const EvenRun& it) { latent_run_f32<DC>(a, e, it, lds); });
+}
+
 // Kernel and work split of a call, from sizes alone.
 struct LatentPlan {
-    int RT;
-    Launch l;
+    AttnSplit split;
+    EvenSplit even;
     size_t bytes;
 };
 LatentPlan plan_of(int T, int B, int Hq, int dc, int max_new, bool bf16_io) {
     const long most = (long)(max_new > 0 && max_new < T ? max_new : T) * Hq;
     LatentPlan p{};
-    p.RT = !bf16_io || most <= 32 ? 1 : most <= 64 ? 2 : 4;
-    p.l = launch_of(T, B, Hq, 1, 32 * p.RT, 10, 9, 8, INT32_MAX);
-    p.bytes = (size_t)p.l.split.slots * p.l.split.R * (dc + 2) * sizeof(float);
+    const int R = !bf16_io || most <= 32 ? 32 : most <= 64 ? 64 : 128;
+    p.split.R = p.even.R = R;
+    p.split.R_log2 = p.even.R_log2 = __builtin_ctz((unsigned)R);
+    p.split.min_rows = 1;
+    p.split.max_rows = INT32_MAX;
+    // as many workgroups as the card's 256 compute units hold
+    p.even.G = dc == 128 ? 512 : 256;
+    p.bytes = (size_t)p.even.G * (2 * R * (dc + 2) + 4) * sizeof(float);
     if (B > kBlock) p.bytes += AttnTable::ints(B) * sizeof(int);
     return p;
 }
 
 template <int DC>
 hipError_t launch(const AttnArgs& a, const LatentPlan& p, hipStream_t st) {
-    const AttnSplit& s = p.l.split;
-    if (a.B > kBlock) attn_list<<<1, 64 * kListWaves, 0, st>>>(a, s, s);
-    const auto run = [&](auto kernel) {
-        in_grids((unsigned)p.l.items, [&](unsigned grid, unsigned first) {
-            kernel<<<grid, kAttnThreads, 0, st>>>(a, s, first);
-        });
-    };
-    if (!a.bf16_io) run(attn_latent_f32<DC>);
-    else if (p.RT == 1) run(attn_latent_bf16<DC, 1>);
-    else if (p.RT == 2) run(attn_latent_bf16<DC, 2>);
-    else run(attn_latent_bf16<DC, 4>);
-    const int n = (int)p.l.joins;
-    if (a.bf16_io) attn_join<bf16, DC><<<(unsigned)n, kAttnThreads, 0, st>>>(a, s, s, n);
-    else attn_join<float, DC><<<(unsigned)n, kAttnThreads, 0, st>>>(a, s, s, n);
+    if (a.B > kBlock) even_list<<<1, 64 * kListWaves, 0, st>>>(a, p.split, p.even);
+    const auto run = [&](auto kernel, int threads) { kernel<<<p.even.G, threads, 0, st>>>(a, p.split, p.even); };
+    if (!a.bf16_io) run(attn_latent_f32<DC>, kAttnThreads);
+    else if (p.split.R == 32) run(attn_latent_bf16<DC, 32>, kLatentThreads);
+    else if (p.split.R == 64) run(attn_latent_bf16<DC, 64>, kLatentThreads);
+    else run(attn_latent_bf16<DC, 128>, kLatentThreads);
+    // no more workgroups than rows of cut tiles
+    const long rows = (long)(p.even.G - 1) * p.split.R;
+    const int n = (int)(rows < kEvenJoins ? rows : kEvenJoins);
+    if (n && a.bf16_io) even_join<bf16, DC><<<n, kAttnThreads, 0, st>>>(a, p.even);
+    else if (n) even_join<float, DC><<<n, kAttnThreads, 0, st>>>(a, p.even);
     return hipGetLastError();
 }
 
@@ -555,11 +629,15 @@ size_t attn_latent_ws(int T, int B, int Hq, int dc, int max_new, bool bf16_io) {
 
 hipError_t launch_attn_latent(const AttnArgs& a, void* ws, hipStream_t st) {
     LatentPlan p = plan_of(a.T, a.B, a.Hq, a.d, a.max_new, a.bf16_io);
-    AttnSplit& s = p.l.split;
-    s.far = LONG_MAX;
-    s.ml = (float*)ws;
-    s.acc = s.ml + (size_t)s.slots * s.R * 2;
-    if (a.B > kBlock) s.table = (int*)(s.acc + (size_t)s.slots * s.R * a.d);
+    EvenSplit& e = p.even;
+    e.pieces = (int*)ws;
+    e.ml = (float*)(e.pieces + 4 * e.G);
+    e.acc = e.ml + (size_t)4 * e.G * e.R;
+    if (a.B > kBlock) e.table = (int*)(e.acc + (size_t)2 * e.G * e.R * a.d);
+    // a call of few keys has fewer units than that
+    const long tiles = ((long)a.T * a.Hq >> e.R_log2) + (a.B < a.T ? a.B : a.T);
+    const long units = tiles * (((long)a.width << a.page_shift) / kUnitKeys + 1 + 2);
+    if (units < e.G) e.G = (int)units;
     switch (a.d) {
         case 128: return launch<128>(a, p, st);
         case 256: return launch<256>(a, p, st);

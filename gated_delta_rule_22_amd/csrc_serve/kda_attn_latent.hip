@@ -58,17 +58,18 @@ template <int KT> struct StepPages {
 // (HV): such a wave makes half the sums of both and adds the other half to one.
 template <int DC, int R_> struct LatentShape {
     static constexpr int W = DC + kPe, R = R_, RP = R / 16;
-    static constexpr int KT = R == 32 ? 64 : 32;     // keys of a step
-    static constexpr int BUF = R == 32 ? 2 : 3;      // steps in LDS
+    static constexpr int KT = 32;                    // keys of a step
+    static constexpr int BUF = R == 128 ? 3 : 4;     // steps in LDS
     static constexpr int HV = R == 128 ? 2 : 1, RTW = HV;
-    static constexpr int RGN = RP / RTW, KG = 8 / RGN / HV;
+    static constexpr int RGN = RP / RTW, KG = R == 128 ? 1 : 2;
+    static constexpr int SW = RGN * KG * HV;         // waves that make scores: 4 or all 8
     static constexpr int NU = KT / 16 / KG;          // key tiles of a wave's scores
     static constexpr int KS = W / 32 / HV;           // steps of their contraction
     static constexpr int CT = DC / 128;              // value columns of a wave, in 16s
     static constexpr int KS2 = KT / 32;
     // Loads of 1 KB: of 16 keys, which one page holds, and the most of a wave. LW waves
     // share 16 keys: wave x of them has the loads from load_of(x) on.
-    static constexpr int LW = 128 / KT, kLoads16 = 16 * (W / 8) / 64, LD = (kLoads16 + LW - 1) / LW;
+    static constexpr int LW = 4, kLoads16 = 16 * (W / 8) / 64, LD = (kLoads16 + LW - 1) / LW;
     static constexpr bool kUneven = kLoads16 % LW != 0;
     __device__ static int load_of(int x) { return kLoads16 * x / LW; }
 };
@@ -93,7 +94,8 @@ __device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e
     constexpr int KS = S::KS, kPieces = W / 8;
     const int wave = wave_id(), lane = threadIdx.x & 63;
     const int c16 = lane & 15, g4 = lane >> 4;
-    const int rg = wave % S::RGN, kg = S::HV > 1 ? 0 : wave / S::RGN, hv = S::HV > 1 ? wave / S::RGN : 0;
+    const int rg = wave % S::RGN, kg = S::HV > 1 ? 0 : wave / S::RGN % S::KG, hv = S::HV > 1 ? wave / S::RGN : 0;
+    const bool scores = S::SW == 8 || wave < S::SW;
     const Keys keys = run_keys(a, it, R);
     const_int* table = table_row(a, it.req);
     const float scale = a.scale * kLog2e;
@@ -191,9 +193,15 @@ __device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e
     }
     int buf = 0;
     for (int pos = keys.begin; pos < keys.end; pos += KT) {
-        // this wave's part of the step has landed; with three buffers the next
-        // step's loads may be in flight, if it has all of them
-        if (BUF == 3 && pos + KT < keys.end && own_page(pg[1]) >= 0) {
+        // this wave's part of the step has landed, what it fetched for later ones may be
+        // in flight
+        int ahead = 0;
+#pragma unroll
+        for (int b = 1; b < BUF - 1; ++b) ahead += pos + b * KT < keys.end && ahead == b - 1 && own_page(pg[b]) >= 0;
+        if (ahead == 2) {
+            if (fewer) wait_loads<2 * LD - 2>();
+            else wait_loads<2 * LD>();
+        } else if (ahead == 1) {
             if (fewer) wait_loads<LD - 1>();
             else wait_loads<LD>();
         } else {
@@ -229,31 +237,34 @@ __device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e
         // scores: kAhead fragments of keys are in flight ahead of their products
         f32x4 sc[RTW], st[NU];
         constexpr int kAhead = KS < 6 ? KS : RTW > 1 ? 4 : 6;
+        float mx = -INFINITY;
+        if (scores) {
 #pragma unroll
-        for (int u = 0; u < NU; ++u) {
-            const bf16* from = tile + (16 * (kg * NU + u) + c16) * W;
-            // pieces first + 4 i + g4: the order of LDS repeats every eight
-            const int first = 4 * KS * hv;
-            const bf16* k[2] = {from + 8 * latent_piece(c16, first + g4), from + 8 * latent_piece(c16, first + 4 + g4)};
-            const auto read = [&](int i) { return *(const bf16x8*)(k[i & 1] + 64 * (i / 2)); };
+            for (int u = 0; u < NU; ++u) {
+                const bf16* from = tile + (16 * (kg * NU + u) + c16) * W;
+                // pieces first + 4 i + g4: the order of LDS repeats every eight
+                const int first = 4 * KS * hv;
+                const bf16* k[2] = {from + 8 * latent_piece(c16, first + g4), from + 8 * latent_piece(c16, first + 4 + g4)};
+                const auto read = [&](int i) { return *(const bf16x8*)(k[i & 1] + 64 * (i / 2)); };
 #pragma unroll
-            for (int rt = 0; rt < RTW; ++rt) sc[rt] = zero4();
-            bf16x8 kf[kAhead];
+                for (int rt = 0; rt < RTW; ++rt) sc[rt] = zero4();
+                bf16x8 kf[kAhead];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) kf[i] = read(i);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < KS; ++i) {
-#pragma unroll
-                for (int rt = 0; rt < RTW; ++rt) sc[rt] = mma32(kf[i % kAhead], qf[rt][i], sc[rt]);
-                if (i + kAhead < KS) kf[i % kAhead] = read(i + kAhead);
+                for (int i = 0; i < kAhead; ++i) kf[i] = read(i);
                 __builtin_amdgcn_sched_barrier(0);
-            }
-            st[u] = sc[0];
-            if constexpr (S::HV > 1) {
-                // to the other half's wave its row tile's sums
-                lds.half[(wave * NU + u) * 64 + lane] = hv ? sc[0] : sc[1];
-                if (hv) st[u] = sc[1];
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+#pragma unroll
+                    for (int rt = 0; rt < RTW; ++rt) sc[rt] = mma32(kf[i % kAhead], qf[rt][i], sc[rt]);
+                    if (i + kAhead < KS) kf[i % kAhead] = read(i + kAhead);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                st[u] = sc[0];
+                if constexpr (S::HV > 1) {
+                    // to the other half's wave its row tile's sums
+                    lds.half[(wave * NU + u) * 64 + lane] = hv ? sc[0] : sc[1];
+                    if (hv) st[u] = sc[1];
+                }
             }
         }
         if constexpr (S::HV > 1) {
@@ -261,48 +272,49 @@ __device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e
 #pragma unroll
             for (int u = 0; u < NU; ++u) st[u] += lds.half[((wave ^ 4) * NU + u) * 64 + lane];
         }
-        for (int u = 0; u < NU; ++u)
-            for (int i = 0; i < 4; ++i) st[u][i] *= scale;
-        if (pos + KT > keys.all || missing) {
+        if (scores) {
             for (int u = 0; u < NU; ++u)
-                for (int i = 0; i < 4; ++i) {
-                    const int y = 16 * (kg * NU + u) + 4 * g4 + i;
-                    if (partial && lds.odd[y]) st[u][i] = NAN;
-                    if (pos + y >= keys.end || (missing >> (kg * NU + u) & 1) || pos + y > limit) st[u][i] = -INFINITY;
-                }
-        }
-        float mx = -INFINITY;
-        for (int u = 0; u < NU; ++u)
-            for (int i = 0; i < 4; ++i) mx = fmaxf(mx, st[u][i]);
-        mx = max_quarters(mx);
-        if constexpr (S::KG > 1) {
-            if (g4 == 0) lds.top[kg][row] = mx;
-            lds_barrier();
-            for (int k = 0; k < S::KG; ++k) mx = fmaxf(mx, lds.top[k][row]);
-        }
-        // The reference may stay behind the maximum by up to 8 in the log2 domain.
-        const bool moved = __any(mx > m + 8.f);
-        if (moved) {
-            const float mn = fmaxf(m, mx);
-            const float c = mn == -INFINITY ? 1.f : exp2_f(m - mn);
-            m = mn;
-            l *= c;
-            if (kg == 0 && g4 == 0) lds.factor[row] = c;
-        }
-        if (kg == 0 && lane == 0) lds.moved[rg * RTW + hv] = moved;
-        const float mu = m == -INFINITY ? 0.f : m;
-        for (int u = 0; u < NU; ++u) {
-            float p[4];
-            for (int i = 0; i < 4; ++i) {
-                p[i] = exp2_f(st[u][i] - mu);
-                l += p[i];
+                for (int i = 0; i < 4; ++i) st[u][i] *= scale;
+            if (pos + KT > keys.all || missing) {
+                for (int u = 0; u < NU; ++u)
+                    for (int i = 0; i < 4; ++i) {
+                        const int y = 16 * (kg * NU + u) + 4 * g4 + i;
+                        if (partial && lds.odd[y]) st[u][i] = NAN;
+                        if (pos + y >= keys.end || (missing >> (kg * NU + u) & 1) || pos + y > limit) st[u][i] = -INFINITY;
+                    }
             }
-            bf16x4 hi, lo;
-            two_terms(p, hi, lo);
-            const int t = kg * NU + u, r = rg * RTW + hv;
-            bf16* to = lds.p + ((r * S::KS2 + t / 2) * 64 + lane) * 8 + 4 * (t & 1);
-            *(bf16x4*)to = hi;
-            *(bf16x4*)(to + S::RP * S::KS2 * 512) = lo;
+            for (int u = 0; u < NU; ++u)
+                for (int i = 0; i < 4; ++i) mx = fmaxf(mx, st[u][i]);
+            mx = max_quarters(mx);
+            if (S::KG > 1 && g4 == 0) lds.top[kg][row] = mx;
+        }
+        if constexpr (S::KG > 1) lds_barrier();
+        if (scores) {
+            for (int k = 0; S::KG > 1 && k < S::KG; ++k) mx = fmaxf(mx, lds.top[k][row]);
+            // The reference may stay behind the maximum by up to 8 in the log2 domain.
+            const bool moved = __any(mx > m + 8.f);
+            if (moved) {
+                const float mn = fmaxf(m, mx);
+                const float c = mn == -INFINITY ? 1.f : exp2_f(m - mn);
+                m = mn;
+                l *= c;
+                if (kg == 0 && g4 == 0) lds.factor[row] = c;
+            }
+            if (kg == 0 && lane == 0) lds.moved[rg * RTW + hv] = moved;
+            const float mu = m == -INFINITY ? 0.f : m;
+            for (int u = 0; u < NU; ++u) {
+                float p[4];
+                for (int i = 0; i < 4; ++i) {
+                    p[i] = exp2_f(st[u][i] - mu);
+                    l += p[i];
+                }
+                bf16x4 hi, lo;
+                two_terms(p, hi, lo);
+                const int t = kg * NU + u, r = rg * RTW + hv;
+                bf16* to = lds.p + ((r * S::KS2 + t / 2) * 64 + lane) * 8 + 4 * (t & 1);
+                *(bf16x4*)to = hi;
+                *(bf16x4*)(to + S::RP * S::KS2 * 512) = lo;
+            }
         }
         lds_barrier();
 
@@ -345,7 +357,7 @@ __device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e
 
     // the rows' sums and references, to all waves
     const float part_sum = sum_quarters(l);
-    if (g4 == 0) {
+    if (scores && g4 == 0) {
         lds.sum[kg][row] = part_sum;
         if (kg == 0) lds.factor[row] = m;
     }

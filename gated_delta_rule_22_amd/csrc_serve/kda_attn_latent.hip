@@ -66,7 +66,7 @@ template <int DC, int R_> struct LatentShape {
     static constexpr int NU = KT / 16 / KG;          // key tiles of a wave's scores
     static constexpr int KS = W / 32 / HV;           // steps of their contraction
     static constexpr int CT = DC / 128;              // value columns of a wave, in 16s
-    static constexpr int KS2 = KT / 32;
+    static constexpr bool kPipe = R > 32;            // see the kernel's loops
     // Loads of 1 KB: of 16 keys, which one page holds, and the most of a wave. LW waves
     // share 16 keys: wave x of them has the loads from load_of(x) on.
     static constexpr int LW = 4, kLoads16 = 16 * (W / 8) / 64, LD = (kLoads16 + LW - 1) / LW;
@@ -78,12 +78,22 @@ constexpr int kLatentThreads = 512;
 template <int DC, int R> struct LatentLds {
     typedef LatentShape<DC, R> S;
     __align__(128) bf16 tile[S::BUF * S::KT * S::W];
-    __align__(16) bf16 p[2 * S::RP * S::KS2 * 64 * 8];
+    __align__(16) bf16 p[2 * S::RP * 64 * 8];
     f32x4 half[S::HV > 1 ? 8 * S::NU * 64 : 1];
     float top[S::KG][R], factor[R], sum[S::KG][R];
     int moved[S::RP], odd[S::KT];
     EvenItem item;
 };
+
+// Largest over the lanes l % 16 + {0, 16, 32, 48}, without LDS.
+__device__ __forceinline__ float max_of_quarters(float x) {
+    const auto u = [](float y) { return __builtin_bit_cast(unsigned, y); };
+    const auto f = [](unsigned y) { return __builtin_bit_cast(float, y); };
+    const auto a = __builtin_amdgcn_permlane16_swap(u(x), u(x), false, false);
+    x = fmaxf(f(a[0]), f(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(u(x), u(x), false, false);
+    return fmaxf(f(b[0]), f(b[1]));
+}
 
 // One run: a piece of a tile's keys, or all of them.
 template <int DC, int R>
@@ -182,143 +192,162 @@ __device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e
         return p;
     };
 
-    StepPages<KT> pg[BUF];                           // of this step and those in flight
-    if (keys.begin < keys.end) {
+    // Steps are fetched in turn; their pages are looked up a fetch earlier. have[b]: of
+    // the b-th step from the next one to be waited for, whether this wave's loads are in
+    // flight (a page that does not exist has none); gaps[b]: its keys without a page.
+    StepPages<KT> next{};
+    if (keys.begin < keys.end) next = pages_at(keys.begin);
+    int fetched = keys.begin, fetch_buf = 0;
+    bool have[BUF] = {};
+    int gaps[BUF] = {};
+    const auto fetch_next = [&](int b) {
+        if (fetched >= keys.end) return;
+        const int page = own_page(next);
+        have[b] = page >= 0;
+        gaps[b] = next.missing();
+        next = pages_at(fetched + KT);
+        fetch(fetch_buf, fetched, page);
+        fetched += KT;
+        fetch_buf = fetch_buf + 1 == BUF ? 0 : fetch_buf + 1;
+    };
+    // Waits for this wave's part of the oldest step; `after` of them are behind it.
+    const auto wait_step = [&](int after) {
+        int n = 0;
 #pragma unroll
-        for (int b = 0; b < BUF - 1; ++b) {
-            pg[b] = pages_at(keys.begin + b * KT);
-            if (keys.begin + b * KT < keys.end) fetch(b, keys.begin + b * KT, own_page(pg[b]));
-        }
-        pg[BUF - 1] = pages_at(keys.begin + (BUF - 1) * KT);
-    }
-    int buf = 0;
-    for (int pos = keys.begin; pos < keys.end; pos += KT) {
-        // this wave's part of the step has landed, what it fetched for later ones may be
-        // in flight
-        int ahead = 0;
-#pragma unroll
-        for (int b = 1; b < BUF - 1; ++b) ahead += pos + b * KT < keys.end && ahead == b - 1 && own_page(pg[b]) >= 0;
-        if (ahead == 2) {
+        for (int b = 1; b < BUF - 1; ++b) n += b <= after && n == b - 1 && have[b];
+        if (n == 2) {
             if (fewer) wait_loads<2 * LD - 2>();
             else wait_loads<2 * LD>();
-        } else if (ahead == 1) {
+        } else if (n == 1) {
             if (fewer) wait_loads<LD - 1>();
             else wait_loads<LD>();
         } else {
             wait_loads<0>();
         }
-        __syncthreads();                             // everybody's, and the last step is done with
-        const int last_buf = buf == 0 ? BUF - 1 : buf - 1;
-        if (pos + (BUF - 1) * KT < keys.end) fetch(last_buf, pos + (BUF - 1) * KT, own_page(pg[BUF - 1]));
-        const int missing = pg[0].missing();
+    };
+    const auto step_done = [&]() {                   // the oldest step is in use
 #pragma unroll
-        for (int b = 0; b < BUF - 1; ++b) pg[b] = pg[b + 1];
-        pg[BUF - 1] = pages_at(pos + BUF * KT);
-        bf16* tile = lds.tile + buf * KT * W;
-        const bool partial = keys.all < keys.end && pos + KT > keys.all;
-        if (partial) {
-            // Positions that only some rows see: a value there that is not finite must
-            // not meet the weight 0 of the others in a product. It counts 0, and the
-            // scores of the rows that see its position become NaN.
-            if (threadIdx.x < KT) lds.odd[threadIdx.x] = 0;
-            __syncthreads();
-            for (int i = 0; i < LD; ++i) {
-                int key, byte;
-                piece_at(i, fresh(lane), key, byte);
-                if ((i == LD - 1 && fewer) || byte >= 2 * DC) continue;
-                bool odd = false;
-                bf16x8* v = (bf16x8*)(tile + 16 * u * W + ((load0 + i) * 64 + lane) * 8);
-                *v = only_finite(*v, odd);
-                if (odd) lds.odd[16 * u + key] = 1;
-            }
-            __syncthreads();
+        for (int b = 0; b + 1 < BUF; ++b) {
+            have[b] = have[b + 1];
+            gaps[b] = gaps[b + 1];
         }
+        have[BUF - 1] = false;
+    };
 
-        // scores: kAhead fragments of keys are in flight ahead of their products
-        f32x4 sc[RTW], st[NU];
-        constexpr int kAhead = KS < 6 ? KS : RTW > 1 ? 4 : 6;
-        float mx = -INFINITY;
-        if (scores) {
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                const bf16* from = tile + (16 * (kg * NU + u) + c16) * W;
-                // pieces first + 4 i + g4: the order of LDS repeats every eight
-                const int first = 4 * KS * hv;
-                const bf16* k[2] = {from + 8 * latent_piece(c16, first + g4), from + 8 * latent_piece(c16, first + 4 + g4)};
-                const auto read = [&](int i) { return *(const bf16x8*)(k[i & 1] + 64 * (i / 2)); };
-#pragma unroll
-                for (int rt = 0; rt < RTW; ++rt) sc[rt] = zero4();
-                bf16x8 kf[kAhead];
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) kf[i] = read(i);
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int i = 0; i < KS; ++i) {
-#pragma unroll
-                    for (int rt = 0; rt < RTW; ++rt) sc[rt] = mma32(kf[i % kAhead], qf[rt][i], sc[rt]);
-                    if (i + kAhead < KS) kf[i % kAhead] = read(i + kAhead);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                st[u] = sc[0];
-                if constexpr (S::HV > 1) {
-                    // to the other half's wave its row tile's sums
-                    lds.half[(wave * NU + u) * 64 + lane] = hv ? sc[0] : sc[1];
-                    if (hv) st[u] = sc[1];
-                }
-            }
+    // Positions that only some rows see: a value there that is not finite must not meet
+    // the weight 0 of the others in a product. It counts 0, and the scores of the rows
+    // that see its position become NaN.
+    const auto clear_odd = [&](bf16* tile) {
+        if (threadIdx.x < KT) lds.odd[threadIdx.x] = 0;
+        __syncthreads();
+        for (int i = 0; i < LD; ++i) {
+            int key, byte;
+            piece_at(i, fresh(lane), key, byte);
+            if ((i == LD - 1 && fewer) || byte >= 2 * DC) continue;
+            bool odd = false;
+            bf16x8* v = (bf16x8*)(tile + 16 * u * W + ((load0 + i) * 64 + lane) * 8);
+            *v = only_finite(*v, odd);
+            if (odd) lds.odd[16 * u + key] = 1;
         }
-        if constexpr (S::HV > 1) {
-            lds_barrier();
+        __syncthreads();
+    };
+
+    // Scores of a step, in three parts with a barrier between the first two: products;
+    // what the other waves have of the rows; weights. kAhead fragments of keys are in
+    // flight ahead of their products.
+    f32x4 st[NU];
+    float mx = -INFINITY;
+    const auto mask = [&](int pos, int missing, bool partial) {
 #pragma unroll
-            for (int u = 0; u < NU; ++u) st[u] += lds.half[((wave ^ 4) * NU + u) * 64 + lane];
-        }
-        if (scores) {
-            for (int u = 0; u < NU; ++u)
-                for (int i = 0; i < 4; ++i) st[u][i] *= scale;
-            if (pos + KT > keys.all || missing) {
-                for (int u = 0; u < NU; ++u)
-                    for (int i = 0; i < 4; ++i) {
-                        const int y = 16 * (kg * NU + u) + 4 * g4 + i;
-                        if (partial && lds.odd[y]) st[u][i] = NAN;
-                        if (pos + y >= keys.end || (missing >> (kg * NU + u) & 1) || pos + y > limit) st[u][i] = -INFINITY;
-                    }
-            }
-            for (int u = 0; u < NU; ++u)
-                for (int i = 0; i < 4; ++i) mx = fmaxf(mx, st[u][i]);
-            mx = max_quarters(mx);
-            if (S::KG > 1 && g4 == 0) lds.top[kg][row] = mx;
-        }
-        if constexpr (S::KG > 1) lds_barrier();
-        if (scores) {
-            for (int k = 0; S::KG > 1 && k < S::KG; ++k) mx = fmaxf(mx, lds.top[k][row]);
-            // The reference may stay behind the maximum by up to 8 in the log2 domain.
-            const bool moved = __any(mx > m + 8.f);
-            if (moved) {
-                const float mn = fmaxf(m, mx);
-                const float c = mn == -INFINITY ? 1.f : exp2_f(m - mn);
-                m = mn;
-                l *= c;
-                if (kg == 0 && g4 == 0) lds.factor[row] = c;
-            }
-            if (kg == 0 && lane == 0) lds.moved[rg * RTW + hv] = moved;
-            const float mu = m == -INFINITY ? 0.f : m;
-            for (int u = 0; u < NU; ++u) {
-                float p[4];
+        for (int x = 0; x < NU; ++x)
+            for (int i = 0; i < 4; ++i) st[x][i] *= scale;
+        if (pos + KT > keys.all || missing) {
+            for (int x = 0; x < NU; ++x)
                 for (int i = 0; i < 4; ++i) {
-                    p[i] = exp2_f(st[u][i] - mu);
-                    l += p[i];
+                    const int y = 16 * (kg * NU + x) + 4 * g4 + i;
+                    if (partial && lds.odd[y]) st[x][i] = NAN;
+                    if (pos + y >= keys.end || (missing >> (kg * NU + x) & 1) || pos + y > limit) st[x][i] = -INFINITY;
                 }
-                bf16x4 hi, lo;
-                two_terms(p, hi, lo);
-                const int t = kg * NU + u, r = rg * RTW + hv;
-                bf16* to = lds.p + ((r * S::KS2 + t / 2) * 64 + lane) * 8 + 4 * (t & 1);
-                *(bf16x4*)to = hi;
-                *(bf16x4*)(to + S::RP * S::KS2 * 512) = lo;
+        }
+        mx = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < NU; ++x)
+            for (int i = 0; i < 4; ++i) mx = fmaxf(mx, st[x][i]);
+        mx = max_of_quarters(mx);
+    };
+    const auto products = [&](const bf16* tile, int pos, int missing, bool partial) {
+        if (!scores) return;
+        constexpr int kAhead = KS < 6 ? KS : RTW > 1 ? 4 : 6;
+#pragma unroll
+        for (int x = 0; x < NU; ++x) {
+            const bf16* from = tile + (16 * (kg * NU + x) + c16) * W;
+            // pieces first + 4 i + g4: the order of LDS repeats every eight
+            const int first = 4 * KS * hv;
+            const bf16* k[2] = {from + 8 * latent_piece(c16, first + g4), from + 8 * latent_piece(c16, first + 4 + g4)};
+            const auto read = [&](int i) { return *(const bf16x8*)(k[i & 1] + 64 * (i / 2)); };
+            f32x4 sc[RTW];
+#pragma unroll
+            for (int rt = 0; rt < RTW; ++rt) sc[rt] = zero4();
+            bf16x8 kf[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) kf[i] = read(i);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+#pragma unroll
+                for (int rt = 0; rt < RTW; ++rt) sc[rt] = mma32(kf[i % kAhead], qf[rt][i], sc[rt]);
+                if (i + kAhead < KS) kf[i % kAhead] = read(i + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            st[x] = sc[0];
+            if constexpr (S::HV > 1) {
+                // to the other half's wave its row tile's sums
+                lds.half[(wave * NU + x) * 64 + lane] = hv ? sc[0] : sc[1];
+                if (hv) st[x] = sc[1];
             }
         }
-        lds_barrier();
-
-        // values
+        if constexpr (S::KG > 1) {
+            mask(pos, missing, partial);
+            if (g4 == 0) lds.top[kg][row] = mx;
+        }
+    };
+    const auto weights = [&](int pos, int missing, bool partial) {
+        if (!scores) return;
+        if constexpr (S::HV > 1) {
+#pragma unroll
+            for (int x = 0; x < NU; ++x) st[x] += lds.half[((wave ^ 4) * NU + x) * 64 + lane];
+            mask(pos, missing, partial);
+        } else {
+#pragma unroll
+            for (int k = 0; k < S::KG; ++k) mx = fmaxf(mx, lds.top[k][row]);
+        }
+        // The reference may stay behind the maximum by up to 8 in the log2 domain.
+        const bool moved = __any(mx > m + 8.f);
+        if (moved) {
+            const float mn = fmaxf(m, mx);
+            const float c = mn == -INFINITY ? 1.f : exp2_f(m - mn);
+            m = mn;
+            l *= c;
+            if (kg == 0 && g4 == 0) lds.factor[row] = c;
+        }
+        if (kg == 0 && lane == 0) lds.moved[rg * RTW + hv] = moved;
+        const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int x = 0; x < NU; ++x) {
+            float p[4];
+            for (int i = 0; i < 4; ++i) {
+                p[i] = exp2_f(st[x][i] - mu);
+                l += p[i];
+            }
+            bf16x4 hi, lo;
+            two_terms(p, hi, lo);
+            const int t = kg * NU + x, r = rg * RTW + hv;
+            bf16* to = lds.p + (r * 64 + lane) * 8 + 4 * t;
+            *(bf16x4*)to = hi;
+            *(bf16x4*)(to + S::RP * 512) = lo;
+        }
+    };
+    const auto values = [&](const bf16* tile) {
         int any_moved = 0;
         for (int r = 0; r < S::RP; ++r) any_moved |= lds.moved[r];
         if (uniform(any_moved)) {
@@ -329,30 +358,75 @@ __device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e
                 for (int b = 0; b < CT; ++b) acc[r][b] *= c;
             }
         }
+        const int key = 4 * g4 + c16 / 4;            // (and 16 behind it: the same order in LDS)
+        bf16x8 va[CT];
 #pragma unroll
-        for (int ks = 0; ks < S::KS2; ++ks) {
-            const int key = 4 * g4 + c16 / 4;        // (and 16 behind it: the same order in LDS)
-            bf16x8 va[CT];
-#pragma unroll
-            for (int b = 0; b < CT; ++b) {
-                // pieces of four b are in four orders, those behind them in the same
-                const int c = 2 * (wave * CT + b % 4) + (c16 & 3) / 2;
-                const bf16* x = tile + key * W + 8 * latent_piece(key, c) + 4 * (c16 & 1) + 64 * (b / 4) + 32 * ks * W;
-                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)x);
-                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(x + 16 * W));
-                va[b] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-            }
-#pragma unroll
-            for (int r = 0; r < S::RP; ++r) {
-                const bf16* x = lds.p + ((r * S::KS2 + ks) * 64 + lane) * 8;
-                const bf16x8 pf = *(const bf16x8*)x, pr = *(const bf16x8*)(x + S::RP * S::KS2 * 512);
-#pragma unroll
-                for (int b = 0; b < CT; ++b) acc[r][b] = mma32(va[b], pf, acc[r][b]);
-#pragma unroll
-                for (int b = 0; b < CT; ++b) acc[r][b] = mma32(va[b], pr, acc[r][b]);
-            }
+        for (int b = 0; b < CT; ++b) {
+            const int c = 2 * (wave * CT + b) + (c16 & 3) / 2;
+            const bf16* x = tile + key * W + 8 * latent_piece(key, c) + 4 * (c16 & 1);
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)x);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(x + 16 * W));
+            va[b] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         }
-        buf = buf + 1 == BUF ? 0 : buf + 1;
+#pragma unroll
+        for (int r = 0; r < S::RP; ++r) {
+            const bf16* x = lds.p + (r * 64 + lane) * 8;
+            const bf16x8 pf = *(const bf16x8*)x, pr = *(const bf16x8*)(x + S::RP * 512);
+#pragma unroll
+            for (int b = 0; b < CT; ++b) acc[r][b] = mma32(va[b], pf, acc[r][b]);
+#pragma unroll
+            for (int b = 0; b < CT; ++b) acc[r][b] = mma32(va[b], pr, acc[r][b]);
+        }
+    };
+
+    const auto tile_of = [&](int b) { return lds.tile + b * KT * W; };
+    if constexpr (S::kPipe) {
+        // The scores of a step are made in front of the values of the one before it, with
+        // no barrier in between: there is always something to multiply. Steps in LDS: two
+        // in use, the others in flight.
+#pragma unroll
+        for (int b = 0; b < BUF - 2; ++b) fetch_next(b);
+        int buf = 0, back = 0;
+        for (int pos = keys.begin; pos < keys.end + KT; pos += KT) {
+            const bool front = pos < keys.end;
+            const bool partial = keys.all < keys.end && pos + KT > keys.all;
+            int missing = 0;
+            if (front) {
+                wait_step(BUF - 3);
+                missing = gaps[0];
+                step_done();
+            }
+            __syncthreads();                         // the step has landed, the weights of the last are there
+            fetch_next(BUF - 3);
+            if (front) {
+                if (partial) clear_odd(tile_of(buf));
+                products(tile_of(buf), pos, missing, partial);
+            }
+            if (pos > keys.begin) values(tile_of(back));
+            lds_barrier();
+            if (front) weights(pos, missing, partial);
+            back = buf;
+            buf = buf + 1 == BUF ? 0 : buf + 1;
+        }
+    } else {
+#pragma unroll
+        for (int b = 0; b < BUF - 1; ++b) fetch_next(b);
+        int buf = 0;
+        for (int pos = keys.begin; pos < keys.end; pos += KT) {
+            const bool partial = keys.all < keys.end && pos + KT > keys.all;
+            wait_step(BUF - 2);
+            const int missing = gaps[0];
+            step_done();
+            __syncthreads();                         // the step has landed, the last one is done with
+            fetch_next(BUF - 2);
+            if (partial) clear_odd(tile_of(buf));
+            products(tile_of(buf), pos, missing, partial);
+            lds_barrier();
+            weights(pos, missing, partial);
+            lds_barrier();
+            values(tile_of(buf));
+            buf = buf + 1 == BUF ? 0 : buf + 1;
+        }
     }
 
     // the rows' sums and references, to all waves

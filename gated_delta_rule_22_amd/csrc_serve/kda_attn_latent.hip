@@ -110,7 +110,7 @@ __device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e
     const_int* table = table_row(a, it.req);
     const float scale = a.scale * kLog2e;
     const int row_mask = (1 << a.page_shift) - 1;
-    const int row = (rg * RTW + hv) * 16 + c16;      // the lane's row of the tile
+    const int row0 = (rg * RTW + hv) * 16, row = row0 + c16;   // the lane's row of the tile
 
     bf16x8 qf[RTW][KS];
 #pragma unroll
@@ -252,12 +252,15 @@ __device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e
         __syncthreads();
     };
 
+    // (what is made from it is made in the step: see fresh)
+    const auto lane_in_step = [&]() { return R < 64 ? lane : fresh(lane); };
     // Scores of a step, in three parts with a barrier between the first two: products;
     // what the other waves have of the rows; weights. kAhead fragments of keys are in
     // flight ahead of their products.
     f32x4 st[NU];
     float mx = -INFINITY;
     const auto mask = [&](int pos, int missing, bool partial) {
+        const int g4 = lane_in_step() >> 4;
 #pragma unroll
         for (int x = 0; x < NU; ++x)
             for (int i = 0; i < 4; ++i) st[x][i] *= scale;
@@ -278,6 +281,7 @@ __device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e
     const auto products = [&](const bf16* tile, int pos, int missing, bool partial) {
         if (!scores) return;
         constexpr int kAhead = KS < 6 ? KS : RTW > 1 ? 4 : 6;
+        const int lane = lane_in_step(), c16 = lane & 15, g4 = lane >> 4;
 #pragma unroll
         for (int x = 0; x < NU; ++x) {
             const bf16* from = tile + (16 * (kg * NU + x) + c16) * W;
@@ -308,18 +312,19 @@ __device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e
         }
         if constexpr (S::KG > 1) {
             mask(pos, missing, partial);
-            if (g4 == 0) lds.top[kg][row] = mx;
+            if (g4 == 0) lds.top[kg][row0 + c16] = mx;
         }
     };
     const auto weights = [&](int pos, int missing, bool partial) {
         if (!scores) return;
+        const int lane = lane_in_step(), c16 = lane & 15, g4 = lane >> 4;
         if constexpr (S::HV > 1) {
 #pragma unroll
             for (int x = 0; x < NU; ++x) st[x] += lds.half[((wave ^ 4) * NU + x) * 64 + lane];
             mask(pos, missing, partial);
         } else {
 #pragma unroll
-            for (int k = 0; k < S::KG; ++k) mx = fmaxf(mx, lds.top[k][row]);
+            for (int k = 0; k < S::KG; ++k) mx = fmaxf(mx, lds.top[k][row0 + c16]);
         }
         // The reference may stay behind the maximum by up to 8 in the log2 domain.
         const bool moved = __any(mx > m + 8.f);
@@ -328,7 +333,7 @@ __device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e
             const float c = mn == -INFINITY ? 1.f : exp2_f(m - mn);
             m = mn;
             l *= c;
-            if (kg == 0 && g4 == 0) lds.factor[row] = c;
+            if (kg == 0 && g4 == 0) lds.factor[row0 + c16] = c;
         }
         if (kg == 0 && lane == 0) lds.moved[rg * RTW + hv] = moved;
         const float mu = m == -INFINITY ? 0.f : m;
@@ -348,6 +353,7 @@ __device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e
         }
     };
     const auto values = [&](const bf16* tile) {
+        const int lane = lane_in_step(), c16 = lane & 15, g4 = lane >> 4;
         int any_moved = 0;
         for (int r = 0; r < S::RP; ++r) any_moved |= lds.moved[r];
         if (uniform(any_moved)) {
@@ -368,14 +374,21 @@ __device__ __forceinline__ void latent_run(const AttnArgs& a, const EvenSplit& e
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(x + 16 * W));
             va[b] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         }
+        // the weights of the next rows are read ahead of these rows' products
+        const bf16* p = lds.p + lane * 8;
+        bf16x8 pf = *(const bf16x8*)p, pr = *(const bf16x8*)(p + S::RP * 512);
 #pragma unroll
         for (int r = 0; r < S::RP; ++r) {
-            const bf16* x = lds.p + (r * 64 + lane) * 8;
-            const bf16x8 pf = *(const bf16x8*)x, pr = *(const bf16x8*)(x + S::RP * 512);
+            const bf16* x = p + (r + 1 < S::RP ? r + 1 : r) * 512;
+            const bf16x8 nf = *(const bf16x8*)x, nr = *(const bf16x8*)(x + S::RP * 512);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int b = 0; b < CT; ++b) acc[r][b] = mma32(va[b], pf, acc[r][b]);
 #pragma unroll
             for (int b = 0; b < CT; ++b) acc[r][b] = mma32(va[b], pr, acc[r][b]);
+            pf = nf;
+            pr = nr;
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
 
@@ -478,6 +491,413 @@ __global__ __launch_bounds__(kLatentThreads, 2) void attn_latent_bf16(
     AttnArgs a, AttnSplit s, EvenSplit e) {
     __shared__ LatentLds<DC, R> lds;
     even_runs(a, s, e, lds.item, [&](const EvenRun& it) { latent_run<DC, R>(a, e, it, lds); });
+}
+
+// The keys of a run on their way to LDS: steps of 32 keys, buffers taken in turn. Each
+// wave loads a part of 16 keys of a step, which one page holds.
+template <int DC, int BUF>
+struct KeySteps {
+    static constexpr int W = DC + kPe, KT = 32, kPieces = W / 8;
+    static constexpr int kLoads16 = 16 * kPieces / 64, LD = (kLoads16 + 3) / 4;
+    static constexpr bool kUneven = kLoads16 % 4 != 0;
+    const AttnArgs& a;
+    const Keys keys;
+    const_int* table;
+    bf16* const tiles;
+    int wave, lane;
+    int half, load0;             // which 16 keys, and the first of the wave's loads of them
+    bool fewer;                  // LD - 1 loads
+    uint32_t off[LD];            // where in the keys' rows the lane's bytes are
+    int fetched, buf;            // the next step's position and buffer
+    int page[2];                 // and pages
+    // of the b-th step from the next one to be waited for: whether loads are in flight (a
+    // page that does not exist has none), and its sixteens without a page
+    bool have[BUF];
+    int gaps[BUF];
+
+    __device__ __forceinline__ KeySteps(const AttnArgs& args, const Keys& k, const_int* t, bf16* to)
+        : a(args), keys(k), table(t), tiles(to), wave(wave_id()), lane(threadIdx.x & 63) {
+        half = wave >> 2;
+        load0 = kLoads16 * (wave & 3) / 4;
+        fewer = kUneven && kLoads16 * ((wave & 3) + 1) / 4 - load0 < LD;
+#pragma unroll
+        for (int i = 0; i < LD; ++i) {
+            int key, byte;
+            piece_at(i, lane, key, byte);
+            off[i] = key * (2 * W) + byte;
+        }
+        fetched = keys.begin;
+        buf = 0;
+#pragma unroll
+        for (int b = 0; b < BUF; ++b) {
+            have[b] = false;
+            gaps[b] = 0;
+        }
+        if (keys.begin < keys.end) look_up();
+    }
+    __device__ __forceinline__ void piece_at(int i, int l, int& key, int& byte) const {
+        const int x = (load0 + i) * 64 + l;
+        key = x / kPieces;
+        byte = 16 * latent_piece(key, x - key * kPieces);
+    }
+    // (sixteens behind the end: the last key's page)
+    __device__ __forceinline__ void look_up() {
+        page[0] = page_at(a, table, min(fetched, keys.end - 1), keys.end);
+        page[1] = page_at(a, table, min(fetched + 16, keys.end - 1), keys.end);
+    }
+    // The next step, b steps behind the next one to be waited for. Positions behind the
+    // end are read from the last one, which some row of the tile sees: nothing else of
+    // an unused row gets here.
+    __device__ __forceinline__ void fetch(int b) {
+        if (fetched >= keys.end) return;
+        const int pg = uniform(half ? page[1] : page[0]);
+        have[b] = pg >= 0;
+        gaps[b] = (page[0] < 0) | (page[1] < 0) << 1;
+        bf16* to = tiles + (buf * KT + 16 * half) * W + load0 * 512;
+        if (pg >= 0) {
+            const int at = uniform(min(fetched + 16 * half, keys.end - 1)), most = keys.end - 1 - at;
+            const int row = at & ((1 << a.page_shift) - 1);
+            const bf16* from = (const bf16*)a.kc + (((long)pg << a.page_shift) + row) * W;
+            const uint32_t l0 = uniform((int)(uint32_t)(uintptr_t)(lds_void*)to);
+            if (most >= 15) {
+#pragma unroll
+                for (int i = 0; i < LD; ++i)
+                    if (i < LD - 1 || !fewer) load_to_lds(l0 + i * 1024, off[i], from);
+            } else {
+                const int l = fresh(lane);
+#pragma unroll
+                for (int i = 0; i < LD; ++i) {
+                    if (i == LD - 1 && fewer) continue;
+                    int key, byte;
+                    piece_at(i, l, key, byte);
+                    load_to_lds(l0 + i * 1024, min(key, most) * (2 * W) + byte, from);
+                }
+            }
+        } else {
+            for (int i = 0; i < LD; ++i)
+                if (i < LD - 1 || !fewer) *(bf16x8*)(to + i * 512 + 8 * lane) = bf16x8{};
+        }
+        fetched += KT;
+        buf = buf + 1 == BUF ? 0 : buf + 1;
+        look_up();
+    }
+    // Waits for this wave's part of the oldest step, of `after` that may be behind it.
+    __device__ __forceinline__ void wait(int after) {
+        int n = 0;
+#pragma unroll
+        for (int b = 1; b < BUF - 1; ++b) n += b <= after && n == b - 1 && have[b];
+        if (n == 2) {
+            if (fewer) wait_loads<2 * LD - 2>();
+            else wait_loads<2 * LD>();
+        } else if (n == 1) {
+            if (fewer) wait_loads<LD - 1>();
+            else wait_loads<LD>();
+        } else {
+            wait_loads<0>();
+        }
+    }
+    // The oldest step is in use; which sixteens of it have no page.
+    __device__ __forceinline__ int take() {
+        const int missing = gaps[0];
+#pragma unroll
+        for (int b = 0; b + 1 < BUF; ++b) {
+            have[b] = have[b + 1];
+            gaps[b] = gaps[b + 1];
+        }
+        have[BUF - 1] = false;
+        return missing;
+    }
+    __device__ __forceinline__ bf16* tile(int b) const { return tiles + b * KT * W; }
+    // Positions that only some rows see: a value there that is not finite must not meet
+    // the weight 0 of the others in a product. It counts 0, and the scores of the rows
+    // that see its position become NaN. By all waves, with barriers.
+    __device__ __forceinline__ void clear_odd(bf16* t, int* odd_keys) const {
+        if (threadIdx.x < KT) odd_keys[threadIdx.x] = 0;
+        __syncthreads();
+        for (int i = 0; i < LD; ++i) {
+            int key, byte;
+            piece_at(i, fresh(lane), key, byte);
+            if ((i == LD - 1 && fewer) || byte >= 2 * DC) continue;
+            bool odd = false;
+            bf16x8* v = (bf16x8*)(t + 16 * half * W + ((load0 + i) * 64 + lane) * 8);
+            *v = only_finite(*v, odd);
+            if (odd) odd_keys[16 * half + key] = 1;
+        }
+        __syncthreads();
+    }
+};
+
+// Tiles of 32 and 64 rows: waves 0 to 3 make the weights, waves 4 to 7 the values of
+// the step before, so that each SIMD has one of both and a step has one barrier. Score
+// wave rg + 2 kg has half of the rows and 16 keys. The rows' reference is what all
+// their keys' maxima were up to the step before: a weight may be up to 2^60 then, which
+// costs nothing in fp32 and bf16. Where a maximum jumps further (the first step of a
+// run, for one), the step's weights are made again behind the barrier.
+template <int DC, int R> struct NarrowLds {
+    static constexpr int W = DC + kPe, RP = R / 16;
+    static constexpr int BUF = R == 64 && DC == 512 ? 3 : 4;     // what LDS holds
+    __align__(128) bf16 tile[BUF * 32 * W];
+    __align__(16) bf16 p[2][2 * RP * 512];
+    float top[2][2][R], factor[2][R], sum[2][R], ref[R];
+    int moved[2][2], jump[2][4], odd[32];
+    EvenItem item;
+};
+constexpr float kJump = 60.f;
+
+template <int DC, int R>
+__device__ __forceinline__ void narrow_run(const AttnArgs& a, const EvenSplit& e, const EvenRun& it,
+                                           NarrowLds<DC, R>& lds) {
+    constexpr int W = DC + kPe, KT = 32, RP = R / 16, RTW = R / 32, KS = W / 32, CT = DC / 64;
+    constexpr int BUF = NarrowLds<DC, R>::BUF;
+    const int wave = wave_id(), lane = threadIdx.x & 63;
+    const int c16 = lane & 15, g4 = lane >> 4;
+    const Keys keys = run_keys(a, it, R);
+    KeySteps<DC, BUF> ks(a, keys, table_row(a, it.req), lds.tile);
+#pragma unroll
+    for (int b = 0; b < BUF - 2; ++b) ks.fetch(b);
+    const int steps = keys.end > keys.begin ? (keys.end - keys.begin + KT - 1) / KT : 0;
+    // (both kinds of waves go through the same barriers)
+    const auto begin_step = [&](int j, bool& partial) {
+        int missing = 0;
+        if (j < steps) {
+            ks.wait(BUF - 3);
+            missing = ks.take();
+        }
+        __syncthreads();                             // the step has landed, the weights of the last are there
+        partial = j < steps && keys.all < keys.end && keys.begin + (j + 1) * KT > keys.all;
+        return missing;
+    };
+    const auto jumped = [&](int j) {
+        const int* x = lds.jump[j & 1];
+        return j >= 0 && uniform(x[0] | x[1] | x[2] | x[3]) != 0;
+    };
+
+    if (wave < 4) {
+        const int rg = wave & 1, kg = wave >> 1, row0 = rg * 16 * RTW + c16;
+        bf16x8 qf[RTW][KS];
+        int limit[RTW];                              // last visible position
+#pragma unroll
+        for (int rt = 0; rt < RTW; ++rt) {
+            const RowAt x = run_row(a, it, it.tile * R + row0 + rt * 16);
+            limit[rt] = x.in ? (int)min((long)it.kept + x.t, (long)kKeepAll) : -1;
+            // (rows behind the request's read its first token's)
+            const bf16* q = (const bf16*)a.q + x.q * W + 8 * g4;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) qf[rt][k] = *(const bf16x8*)(q + 32 * k);
+        }
+        const float scale = a.scale * kLog2e;
+        float m[RTW], l[RTW], l_before[RTW], factor[RTW];
+        f32x4 st[RTW];
+#pragma unroll
+        for (int rt = 0; rt < RTW; ++rt) {
+            m[rt] = -INFINITY;
+            l[rt] = l_before[rt] = 0.f;
+            factor[rt] = 1.f;
+            st[rt] = zero4();
+        }
+        const auto weights = [&](int j) {
+#pragma unroll
+            for (int rt = 0; rt < RTW; ++rt) {
+                const float mu = m[rt] == -INFINITY ? 0.f : m[rt];
+                float p[4];
+                l_before[rt] = l[rt];
+                for (int i = 0; i < 4; ++i) {
+                    p[i] = exp2_f(st[rt][i] - mu);
+                    l[rt] += p[i];
+                }
+                bf16x4 hi, lo;
+                two_terms(p, hi, lo);
+                bf16* to = lds.p[j & 1] + ((rg * RTW + rt) * 64 + lane) * 8 + 4 * kg;
+                *(bf16x4*)to = hi;
+                *(bf16x4*)(to + RP * 512) = lo;
+            }
+        };
+        // The rows' largest score of step j, of both key groups.
+        const auto top_of = [&](int j, int rt) {
+            return fmaxf(lds.top[j & 1][0][row0 + rt * 16], lds.top[j & 1][1][row0 + rt * 16]);
+        };
+        const auto follow = [&](int rt, float top) {
+            const float mn = fmaxf(m[rt], top), c = mn == -INFINITY ? 1.f : exp2_f(m[rt] - mn);
+            m[rt] = mn;
+            l[rt] *= c;
+            factor[rt] *= c;
+        };
+        const auto publish = [&](int j, bool moved) {
+            if (kg != 0) return;
+            if (moved && g4 == 0)
+#pragma unroll
+                for (int rt = 0; rt < RTW; ++rt) lds.factor[j & 1][row0 + rt * 16] = factor[rt];
+            if (lane == 0) lds.moved[j & 1][rg] = moved;
+        };
+        int buf = 0;
+        for (int j = 0; j <= steps; ++j) {
+            bool partial;
+            const int missing = begin_step(j, partial);
+            if (jumped(j - 1)) {
+#pragma unroll
+                for (int rt = 0; rt < RTW; ++rt) {
+                    l[rt] = l_before[rt];
+                    follow(rt, top_of(j - 1, rt));
+                }
+                publish(j - 1, true);
+                weights(j - 1);
+                __syncthreads();
+            }
+            ks.fetch(BUF - 3);
+            if (partial) ks.clear_odd(ks.tile(buf), lds.odd);
+            if (j == steps) break;
+            // The reference may stay behind the maximum by up to 8 in the log2 domain.
+            float top[RTW];
+            bool ahead = false;
+#pragma unroll
+            for (int rt = 0; rt < RTW; ++rt) {
+                factor[rt] = 1.f;
+                top[rt] = j > 0 ? top_of(j - 1, rt) : -INFINITY;
+                ahead |= top[rt] > m[rt] + 8.f;
+            }
+            const bool moved = __any(ahead);
+            if (moved) {
+#pragma unroll
+                for (int rt = 0; rt < RTW; ++rt) follow(rt, top[rt]);
+            }
+            publish(j, moved);
+
+            // products: fragments of keys are in flight ahead of them
+            const bf16* from = ks.tile(buf) + (16 * kg + c16) * W;
+            // (pieces 4 i + g4: the order of LDS repeats every eight)
+            const bf16* k[2] = {from + 8 * latent_piece(c16, g4), from + 8 * latent_piece(c16, 4 + g4)};
+            const auto read = [&](int i) { return *(const bf16x8*)(k[i & 1] + 64 * (i / 2)); };
+            constexpr int kAhead = KS < 6 ? KS : 6;
+            bf16x8 kf[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) kf[i] = read(i);
+#pragma unroll
+            for (int rt = 0; rt < RTW; ++rt) st[rt] = zero4();
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+#pragma unroll
+                for (int rt = 0; rt < RTW; ++rt) st[rt] = mma32(kf[i % kAhead], qf[rt][i], st[rt]);
+                if (i + kAhead < KS) kf[i % kAhead] = read(i + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const int pos = keys.begin + j * KT;
+            bool jump = false;
+#pragma unroll
+            for (int rt = 0; rt < RTW; ++rt) {
+                for (int i = 0; i < 4; ++i) st[rt][i] *= scale;
+                if (pos + KT > keys.all || missing) {
+                    for (int i = 0; i < 4; ++i) {
+                        const int y = 16 * kg + 4 * g4 + i;
+                        if (partial && lds.odd[y]) st[rt][i] = NAN;
+                        if (pos + y >= keys.end || (missing >> kg & 1) || pos + y > limit[rt]) st[rt][i] = -INFINITY;
+                    }
+                }
+                const float mx = max_of_quarters(fmaxf(fmaxf(st[rt][0], st[rt][1]), fmaxf(st[rt][2], st[rt][3])));
+                if (g4 == 0) lds.top[j & 1][kg][row0 + rt * 16] = mx;
+                jump |= mx > m[rt] + kJump;
+            }
+            jump = __any(jump);
+            if (lane == 0) lds.jump[j & 1][wave] = jump;
+            weights(j);
+            buf = buf + 1 == BUF ? 0 : buf + 1;
+        }
+#pragma unroll
+        for (int rt = 0; rt < RTW; ++rt) {
+            const float sum = sum_quarters(l[rt]);
+            if (g4 == 0) {
+                lds.sum[kg][row0 + rt * 16] = sum;
+                if (kg == 0) lds.ref[row0 + rt * 16] = m[rt];
+            }
+        }
+        __syncthreads();
+        return;
+    }
+
+    const int vw = wave - 4;
+    f32x4 acc[RP][CT];
+#pragma unroll
+    for (int r = 0; r < RP; ++r)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[r][c] = zero4();
+    int buf = 0, back = 0;
+    for (int j = 0; j <= steps; ++j) {
+        bool partial;
+        begin_step(j, partial);
+        if (jumped(j - 1)) __syncthreads();          // the weights are made again
+        ks.fetch(BUF - 3);
+        if (partial) ks.clear_odd(ks.tile(buf), lds.odd);
+        if (j > 0) {
+            const int x = (j - 1) & 1;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (!uniform(lds.moved[x][g])) continue;
+#pragma unroll
+                for (int rt = 0; rt < RTW; ++rt) {
+                    const float c = lds.factor[x][(g * RTW + rt) * 16 + c16];
+#pragma unroll
+                    for (int b = 0; b < CT; ++b) acc[g * RTW + rt][b] *= c;
+                }
+            }
+            const bf16* tile = ks.tile(back);
+            const int key = 4 * g4 + c16 / 4;        // (and 16 behind it: the same order in LDS)
+            bf16x8 va[CT];
+#pragma unroll
+            for (int b = 0; b < CT; ++b) {
+                // pieces of four b are in four orders, those behind them in the same
+                const int c = 2 * (vw * CT + b % 4) + (c16 & 3) / 2;
+                const bf16* v = tile + key * W + 8 * latent_piece(key, c) + 4 * (c16 & 1) + 64 * (b / 4);
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)v);
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + 16 * W));
+                va[b] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            }
+            const bf16* p = lds.p[x] + lane * 8;
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+                const bf16x8 pf = *(const bf16x8*)(p + r * 512), pr = *(const bf16x8*)(p + (RP + r) * 512);
+#pragma unroll
+                for (int b = 0; b < CT; ++b) acc[r][b] = mma32(va[b], pf, acc[r][b]);
+#pragma unroll
+                for (int b = 0; b < CT; ++b) acc[r][b] = mma32(va[b], pr, acc[r][b]);
+            }
+        }
+        back = buf;
+        buf = buf + 1 == BUF ? 0 : buf + 1;
+    }
+    __syncthreads();                                 // the rows' sums and references are there
+    const int col = vw * (16 * CT) + 4 * g4;
+#pragma unroll
+    for (int r = 0; r < RP; ++r) {
+        const int y = 16 * r + c16;
+        const float sum = lds.sum[0][y] + lds.sum[1][y], ref = lds.ref[y];
+        if (it.pieces > 1) {
+            const long at = (long)it.slot * R + y;
+            // (a row without a key in this piece has l = 0, and its values are not used)
+#pragma unroll
+            for (int b = 0; b < CT; ++b) *(f32x4*)(e.acc + at * DC + col + 16 * b) = acc[r][b];
+            if (vw == 0 && g4 == 0) {
+                e.ml[at * 2] = ref;
+                e.ml[at * 2 + 1] = sum;
+            }
+            continue;
+        }
+        const RowAt x = run_row(a, it, it.tile * R + y);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (!x.in) continue;
+#pragma unroll
+        for (int b = 0; b < CT; ++b) {
+            bf16x4 z;
+            for (int i = 0; i < 4; ++i) z[i] = (bf16)(acc[r][b][i] * inv);
+            *(bf16x4*)((bf16*)a.o + x.q * DC + col + 16 * b) = z;
+        }
+        if (a.lse && vw == 0 && g4 == 0) a.lse[x.q] = sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * kLn2;
+    }
+}
+
+template <int DC, int R>
+__global__ __launch_bounds__(kLatentThreads, 2) void attn_latent_narrow(AttnArgs a, AttnSplit s, EvenSplit e) {
+    __shared__ NarrowLds<DC, R> lds;
+    even_runs(a, s, e, lds.item, [&](const EvenRun& it) { narrow_run<DC, R>(a, e, it, lds); });
 }
 
 // fp32: 32 rows, 32 keys a step. Scores: a wave takes 16 rows and 16 keys, lane
@@ -696,8 +1116,8 @@ hipError_t launch(const AttnArgs& a, const LatentPlan& p, hipStream_t st) {
     if (a.B > kBlock) even_list<<<1, 64 * kListWaves, 0, st>>>(a, p.split, p.even);
     const auto run = [&](auto kernel, int threads) { kernel<<<p.even.G, threads, 0, st>>>(a, p.split, p.even); };
     if (!a.bf16_io) run(attn_latent_f32<DC>, kAttnThreads);
-    else if (p.split.R == 32) run(attn_latent_bf16<DC, 32>, kLatentThreads);
-    else if (p.split.R == 64) run(attn_latent_bf16<DC, 64>, kLatentThreads);
+    else if (p.split.R == 32) run(attn_latent_narrow<DC, 32>, kLatentThreads);
+    else if (p.split.R == 64) run(attn_latent_narrow<DC, 64>, kLatentThreads);
     else run(attn_latent_bf16<DC, 128>, kLatentThreads);
     // no more workgroups than rows of cut tiles
     const long rows = (long)(p.even.G - 1) * p.split.R;

@@ -1,14 +1,16 @@
 // Work split for attention kernels of which a compute unit holds one workgroup:
-// G workgroups, each an even share of the call's keys.
+// G groups of workgroups, each an even share of the call's keys.
 //
-// The rows of a request are cut into tiles of R as in kda_attn_sched.h (one KV head).
-// A tile is a number of units: its keys in Cs, behind `start` units without keys
-// that stand for what beginning a tile costs. The units of all tiles in a row,
-// cut into G ranges of equal length, are the workgroups' work: whole tiles, and at
-// either end of a range a piece of one that neighbours have the rest of. (Parts of
-// one length, dealt out to the compute units in turn, left some of them a third more
-// to do than others: 256 requests over 1024 to 32768 positions, 1015 us.) Every
-// workgroup finds its range from the lengths on the device.
+// The rows of a request are cut into tiles of R times `side` rows as in
+// kda_attn_sched.h (one KV head). A tile is a number of units: its keys in Cs, behind
+// `start` units without keys that stand for what beginning it costs. The units of all
+// tiles in a row, cut into G ranges of equal length, are the groups' work: whole
+// tiles, and at either end of a range a piece of one that neighbours have the rest of.
+// (Parts of one length, dealt out to the compute units in turn, left some of them a third
+// more to do than others.) Every workgroup finds its range from the lengths on the device.
+//
+// A group is `side` workgroups, each with R rows of its tiles: they read the same keys
+// at the same time, on the same XCD, in whose cache all but the first find them.
 //
 // A piece's rows go to the workspace, at most two pieces a workgroup, and a second
 // kernel joins them. The workgroup that has a tile's second piece describes the
@@ -21,13 +23,14 @@ namespace kda {
 namespace {
 
 struct EvenSplit {
-    int R, R_log2;
-    int G;              // workgroups
+    int R;              // rows of a workgroup; AttnSplit has those of a tile
+    int side;           // workgroups side by side
+    int G;              // groups of them
     int* table;         // of more than kBlock requests: see AttnTable; null otherwise
-    int* pieces;        // [G][4]: first row, tile, new tokens, pieces (0: none) of the tile whose
-                        // second piece this workgroup has
-    float* ml;          // [2 G][R][2]: running maximum (log2 domain), sum
-    float* acc;         // [2 G][R][d]: unnormalised rows
+    int* pieces;        // [G side][4]: first row, tile of R rows, new tokens, pieces (0: none) of
+                        // the tile whose second piece this workgroup has
+    float* ml;          // [2 G side][R][2]: running maximum (log2 domain), sum
+    float* acc;         // [2 G side][R][d]: unnormalised rows
 };
 
 // Keys of a unit: 64, or what makes the call some 2^16 units. (cost: tiles times keys,
@@ -144,7 +147,7 @@ struct EvenRun {
     int req, tile, row0, n, kept;
     int begin, end;     // keys (end: not cut at the request's length)
     int piece, pieces;
-    int slot;           // of a piece
+    int slot;           // of a piece: the group's first run has even ones, its last odd ones
     int units;          // the run's
 };
 __device__ __forceinline__ EvenRun even_run(const EvenItem& lds, const EvenSplit& e, int w, int y, int y1) {
@@ -165,7 +168,7 @@ __device__ __forceinline__ EvenRun even_run(const EvenItem& lds, const EvenSplit
     const int w0 = (int)(((first + 1) * G - 1) / total), w1 = (int)(((last + 1) * G - 1) / total);
     r.piece = w - w0;   // below 0: of this tile only units without keys
     r.pieces = w1 - w0 + 1;
-    r.slot = r.piece > 0 ? 2 * w : 2 * w + 1;
+    r.slot = r.piece > 0 ? 0 : 1;
     return r;
 }
 
@@ -192,7 +195,9 @@ __device__ __forceinline__ RowAt run_row(const AttnArgs& a, const EvenRun& it, i
 // A workgroup's runs in turn, each with what is left in LDS free to use.
 template <typename A, typename F>
 __device__ __forceinline__ void even_runs(const A& a, const AttnSplit& s, const EvenSplit& e, EvenItem& item, F run) {
-    const int w = blockIdx.x;
+    // workgroups go to the 8 XCDs in turn: neighbours in the units on the same one
+    const int n = gridDim.x, b = blockIdx.x, v = n % 8 ? b : b % 8 * (n / 8) + b / 8;
+    const int w = v / e.side, side = v - w * e.side;
     int y = -1, y1 = 0;
     for (;;) {
         if (wave_id() == 0) even_find(a, s, e, y, w, &item);
@@ -203,19 +208,22 @@ __device__ __forceinline__ void even_runs(const A& a, const AttnSplit& s, const 
             y = even_begin(e, total, w);
             y1 = even_begin(e, total, w + 1);
         }
-        const bool more = y < y1 && uniform((int)item.found) != 0;
+        bool more = y < y1 && uniform((int)item.found) != 0;
         EvenRun it{};
         if (more) it = even_run(item, e, w, y, y1);
+        it.tile = it.tile * e.side + side;
+        it.slot += 2 * v;
+        const bool rows = it.tile * e.R < it.n * a.Hq;
         if (first && threadIdx.x == 0) {
-            int* x = e.pieces + 4 * w;
+            int* x = e.pieces + 4 * v;
             x[0] = it.row0;
             x[1] = it.tile;
             x[2] = it.n;
-            x[3] = more && it.piece == 1 ? it.pieces : 0;
+            x[3] = more && rows && it.piece == 1 ? it.pieces : 0;
         }
         if (!more) return;
         y += it.units;
-        if (it.piece >= 0) run(it);
+        if (it.piece >= 0 && rows) run(it);
         __syncthreads();                             // the run's last reads of LDS are done
     }
 }
@@ -290,7 +298,7 @@ __global__ __launch_bounds__(kAttnThreads) void even_join(A a, EvenSplit e) {
         for (int i = 0; i < 2; ++i) {
             const int w = 2 * (int)threadIdx.x + i;
             mine[i] = 0;
-            if (w >= e.G) continue;
+            if (w >= e.G * e.side) continue;
             const i32x4 x = *(const i32x4*)(e.pieces + 4 * w);
             if (x[3] > 0) mine[i] = max(min(e.R, x[2] * a.Hq - x[1] * e.R), 0);
         }
@@ -322,11 +330,13 @@ __global__ __launch_bounds__(kAttnThreads) void even_join(A a, EvenSplit e) {
         const i32x4 x = *(const i32x4*)(e.pieces + 4 * w);
         const int row_a = r - from, have = end - r, pieces = x[3];
         r = end;
-        // pieces of workgroups w - 1 (its last run), w, w + 1, ... (their first ones)
-        if (w < 1 || w - 1 + pieces > e.G) continue;   // (a guard)
+        // pieces of the group before this one (its last run), this one's, the next one's, ...
+        // (their first ones)
+        const int v0 = w - e.side;
+        if (v0 < 0 || v0 + (pieces - 1) * e.side >= e.G * e.side) continue;   // (a guard)
         const auto part = [&](int row, int p) {
             const bool in = p < pieces;
-            const int slot = !in || p == 0 ? 2 * (w - 1) + 1 : 2 * (w - 1 + p);
+            const int slot = !in || p == 0 ? 2 * v0 + 1 : 2 * (v0 + p * e.side);
             const long at = (long)slot * e.R + row;
             Joined y;
             y.m = e.ml[at * 2];

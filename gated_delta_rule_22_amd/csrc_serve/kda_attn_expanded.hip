@@ -14,34 +14,38 @@
 namespace kda {
 namespace {
 
-// 16 bytes a lane, each from an address of its own, to LDS at the wave's address
-// `to`, in the order of the lanes.
-__device__ __forceinline__ void load_to_lds_at(uint32_t to, const char* from) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                 ::"s"(to), "v"(from) : "memory", "m0");
-}
-
-// A wave's share of the loads of a step: its keys' rows as they lie in LDS. Piece
-// c of LDS row r is 16 bytes that `source` names.
-template <int LD>
+// A wave's share of the loads of a step: KEYS rows of 16 P bytes, key by key as they
+// lie in LDS.
+template <int KEYS, int P>
 struct KeyLoads {
-    const char* p[LD];           // the lane's bytes of the step ahead
-    long stride[LD];             // from one key to the next
-    int key[LD];                 // of the wave's keys
+    static constexpr int LD = KEYS * P / 64;
+    const char* base;            // the wave's first key of the step ahead
+    long stride;                 // bytes from one key to the next, at most 2^28
+    uint32_t off[LD];            // the lane's bytes
 
-    // of a step of which `have` of the wave's keys exist (at least 1: others read
-    // the last one), to LDS at `to`
-    __device__ __forceinline__ void issue(uint32_t to, int have, int keys, int step) {
-        if (have >= keys) {
+    static __device__ __forceinline__ int key(int i) { return (i * 64 + (threadIdx.x & 63)) / P; }
+    // `place`: the 16 bytes of a key's row that lie in its piece c
+    template <typename F>
+    __device__ __forceinline__ void init(const char* from, long bytes, F place) {
+        base = from;
+        stride = bytes;
+        for (int i = 0; i < LD; ++i)
+            off[i] = (uint32_t)(key(i) * stride) + 16 * place(key(i), (int)(threadIdx.x & 63) % P);
+    }
+    // of a step of which `have` of the wave's keys exist (others read the last one that
+    // does, which may be another wave's), to LDS at `to`
+    __device__ __forceinline__ void issue(uint32_t to, int have, int step) {
+        if (have >= KEYS) {
 #pragma unroll
-            for (int i = 0; i < LD; ++i) load_to_lds_at(to + i * 1024, p[i]);
+            for (int i = 0; i < LD; ++i) load_to_lds(to + i * 1024, off[i], base);
         } else {
+            const char* from = base + min(have - 1, 0) * stride;
+            const int last = max(have - 1, 0);
 #pragma unroll
             for (int i = 0; i < LD; ++i)
-                load_to_lds_at(to + i * 1024, p[i] + (min(key[i], have - 1) - key[i]) * stride[i]);
+                load_to_lds(to + i * 1024, off[i] - (uint32_t)((key(i) - min(key(i), last)) * stride), from);
         }
-#pragma unroll
-        for (int i = 0; i < LD; ++i) p[i] += stride[i] * step;
+        base += stride * step;
     }
 };
 
@@ -53,14 +57,14 @@ template <int DV> struct ExpandedShape {
 
 template <int DV> struct ExpandedLds {
     typedef ExpandedShape<DV> S;
-    __align__(128) bf16 k[2 * S::KT * S::DK], v[2 * S::KT * DV];
+    __align__(128) bf16 k[2 * S::KT * DV], pe[2 * S::KT * kPe], v[2 * S::KT * DV];
     int odd_wave[S::kWaves];
     AttnItem item;
 };
 
-// LDS order of a key's pieces: reads of one piece of 16 keys cover the banks.
-template <int DK> __device__ __forceinline__ int expanded_piece(int key, int c) {
-    return DK % 128 == 0 ? c ^ (key & 15) : c ^ (key >> 1 & 7);
+// LDS order of a key's pieces of D channels: reads of one piece of 16 keys cover the banks.
+template <int D> __device__ __forceinline__ int expanded_piece(int key, int c) {
+    return D == 128 ? c ^ (key & 15) : c ^ (key >> 1 & 7);
 }
 
 template <int DV>
@@ -68,8 +72,7 @@ __global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, 2) void attn_expand
     ExpandedArgs a, AttnSplit s, unsigned first_block) {
     typedef ExpandedShape<DV> S;
     constexpr int DK = S::DK, KT = S::KT, KS = DK / 16, NB = DV / 32, kKeys = S::kKeys;
-    constexpr int KP = DK / 8, VP = DV / 8;          // pieces of a row
-    constexpr int LK = kKeys * KP / 64, LV = kKeys * VP / 64;
+    constexpr int LV = kKeys * DV / 512;
     __shared__ ExpandedLds<DV> lds;
     const AttnItem it = attn_item(a, s, (int)(first_block + blockIdx.x), lds.item);
     if (!it.found) return;
@@ -77,7 +80,7 @@ __global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, 2) void attn_expand
     const int c32 = lane & 31, half = lane >> 5;
     const Keys keys = part_keys(a, s, it, 1);
     const float scale = a.scale * kLog2e;
-    const long k0 = a.row_of(it.req);
+    const long k0 = uniform(a.row_of(it.req));
     const long kv_row = (long)a.Hq * 2 * DV;         // dn = dv
     const bf16* kv = (const bf16*)a.kc + k0 * kv_row + (long)it.h * 2 * DV;
     const bf16* pe = (const bf16*)a.vc + k0 * a.pe_stride;
@@ -86,7 +89,8 @@ __global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, 2) void attn_expand
     const RowAt at = row_at(a, it, 1, it.tile * s.R + wave * 32 + c32);
     const int limit = at.in ? (int)min((long)it.kept + at.t, (long)kKeepAll) : INT_MIN;
     // last position that a row of this wave sees
-    const int wave_limit = uniform((int)min((long)it.kept + it.tile * s.R + wave * 32 + 31, (long)kKeepAll));
+    const int first_row = it.tile * s.R + wave * 32;
+    const int wave_limit = first_row < it.n ? uniform((int)min((long)it.kept + first_row + 31, (long)kKeepAll)) : -1;
     for (int k = 0; k < KS; ++k) {
         bf16x8 z = {};
         if (at.in) z = *(const bf16x8*)((const bf16*)a.q + at.q * DK + 8 * half + 16 * k);
@@ -96,30 +100,20 @@ __global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, 2) void attn_expand
     f32x16 acc[NB];
     for (int b = 0; b < NB; ++b) acc[b] = f32x16{};
 
-    KeyLoads<LK> kl;
-    KeyLoads<LV> vl;
-    const long begin = keys.begin + wave * kKeys;
-    for (int i = 0; i < LK; ++i) {
-        const int x = i * 64 + lane, r = x / KP, c = expanded_piece<DK>(wave * kKeys + r, x % KP);
-        const bool own = c < DV / 8;
-        kl.key[i] = r;
-        kl.stride[i] = 2 * (own ? kv_row : a.pe_stride);
-        kl.p[i] = (const char*)(own ? kv + 8 * c : pe + 8 * (c - DV / 8)) + (begin + r) * kl.stride[i];
-    }
-    for (int i = 0; i < LV; ++i) {
-        const int x = i * 64 + lane, r = x / VP, c = v_piece4<DV>(wave * kKeys + r, x % VP);
-        vl.key[i] = r;
-        vl.stride[i] = 2 * kv_row;
-        vl.p[i] = (const char*)(kv + DV + 8 * c) + (begin + r) * vl.stride[i];
-    }
+    const int k_first = wave * kKeys;                // of the keys that this wave fetches
+    const char* kv_at = (const char*)(kv + (long)(keys.begin + k_first) * kv_row);
+    KeyLoads<kKeys, DV / 8> kl, vl;
+    KeyLoads<kKeys, kPe / 8> pl;
+    kl.init(kv_at, 2 * kv_row, [&](int r, int c) { return expanded_piece<DV>(k_first + r, c); });
+    pl.init((const char*)(pe + (long)(keys.begin + k_first) * a.pe_stride), 2 * a.pe_stride,
+            [&](int r, int c) { return expanded_piece<kPe>(k_first + r, c); });
+    vl.init(kv_at + 2 * DV, 2 * kv_row, [&](int r, int c) { return v_piece4<DV>(k_first + r, c); });
     const auto address = [&](bf16* p) { return (uint32_t)uniform((int)(uint32_t)(uintptr_t)(lds_void*)p); };
-    // a wave none of whose keys exist reads those of the last key
-    auto fetch = [&](int buf, int pos) {
-        const int have = keys.end - (pos + wave * kKeys);
-        const uint32_t tk = address(lds.k + (buf * KT + wave * kKeys) * DK);
-        const uint32_t tv = address(lds.v + (buf * KT + wave * kKeys) * DV);
-        kl.issue(tk, have, kKeys, KT);
-        vl.issue(tv, have, kKeys, KT);
+    const auto fetch = [&](int buf, int pos) {
+        const int have = keys.end - (pos + k_first);
+        kl.issue(address(lds.k + (buf * KT + k_first) * DV), have, KT);
+        pl.issue(address(lds.pe + (buf * KT + k_first) * kPe), have, KT);
+        vl.issue(address(lds.v + (buf * KT + k_first) * DV), have, KT);
     };
 
     if (keys.begin < keys.end) fetch(0, keys.begin);
@@ -128,7 +122,7 @@ __global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, 2) void attn_expand
         __builtin_amdgcn_s_waitcnt(0x0f70);          // vmcnt(0): this wave's part has landed
         __syncthreads();
         if (pos + KT < keys.end) fetch(buf ^ 1, pos + KT);
-        const bf16* kt = lds.k + buf * KT * DK;
+        const bf16 *kt = lds.k + buf * KT * DV, *pt = lds.pe + buf * KT * kPe;
         bf16* vt = lds.v + buf * KT * DV;
         bool odd = false;
         if (pos + KT > keys.all) {
@@ -154,7 +148,9 @@ __global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, 2) void attn_expand
             st[u] = f32x16{};
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                const bf16x8 kf = *(const bf16x8*)(kt + (32 * u + c32) * DK + 8 * expanded_piece<DK>(c32, 2 * k + half));
+                const bf16x8 kf = k < DV / 16
+                    ? *(const bf16x8*)(kt + (32 * u + c32) * DV + 8 * expanded_piece<DV>(c32, 2 * k + half))
+                    : *(const bf16x8*)(pt + (32 * u + c32) * kPe + 8 * expanded_piece<kPe>(c32, 2 * k - DV / 8 + half));
                 st[u] = mma_big(kf, qf[k], st[u]);
             }
         }
@@ -261,7 +257,7 @@ __global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, 2) void attn_expand
 // the 16 columns of a product's block of values are 4 apart.
 template <int DV> struct ExpandedLdsF {
     static constexpr int DK = DV + kPe, KT = 16;
-    __align__(128) float k[2 * KT * DK], v[2 * KT * DV];
+    __align__(128) float k[2 * KT * DV], pe[2 * KT * kPe], v[2 * KT * DV];
     int odd_wave[4];
     AttnItem item;
 };
@@ -271,7 +267,7 @@ template <int DV>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_expanded_f32(ExpandedArgs a, AttnSplit s,
                                                                      unsigned first_block) {
     constexpr int DK = DV + kPe, KT = 16, KQ = DK / 16, CT = DV / 16, kKeys = KT / 4;
-    constexpr int KP = DK / 4, VP = DV / 4, LK = kKeys * KP / 64, LV = kKeys * VP / 64;
+    constexpr int LV = kKeys * DV / 256;
     __shared__ ExpandedLdsF<DV> lds;
     const AttnItem it = attn_item(a, s, (int)(first_block + blockIdx.x), lds.item);
     if (!it.found) return;
@@ -279,7 +275,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_expanded_f32(ExpandedArg
     const int c16 = lane & 15, g4 = lane >> 4;
     const Keys keys = part_keys(a, s, it, 1);
     const float scale = a.scale * kLog2e;
-    const long k0 = a.row_of(it.req);
+    const long k0 = uniform(a.row_of(it.req));
     const long kv_row = (long)a.Hq * 2 * DV;
     const float* kv = (const float*)a.kc + k0 * kv_row + (long)it.h * 2 * DV;
     const float* pe = (const float*)a.vc + k0 * a.pe_stride;
@@ -298,27 +294,20 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_expanded_f32(ExpandedArg
     f32x4 acc[CT];
     for (int b = 0; b < CT; ++b) acc[b] = zero4();
 
-    KeyLoads<LK> kl;
-    KeyLoads<LV> vl;
-    const long begin = keys.begin + wave * kKeys;
-    for (int i = 0; i < LK; ++i) {
-        const int x = i * 64 + lane, r = x / KP, c = piece(wave * kKeys + r, x % KP);
-        const bool own = c < DV / 4;
-        kl.key[i] = r;
-        kl.stride[i] = 4 * (own ? kv_row : a.pe_stride);
-        kl.p[i] = (const char*)(own ? kv + 4 * c : pe + 4 * (c - DV / 4)) + (begin + r) * kl.stride[i];
-    }
-    for (int i = 0; i < LV; ++i) {
-        const int x = i * 64 + lane, r = x / VP, c = x % VP;
-        vl.key[i] = r;
-        vl.stride[i] = 4 * kv_row;
-        vl.p[i] = (const char*)(kv + DV + 4 * c) + (begin + r) * vl.stride[i];
-    }
+    const int k_first = wave * kKeys;
+    const char* kv_at = (const char*)(kv + (long)(keys.begin + k_first) * kv_row);
+    KeyLoads<kKeys, DV / 4> kl, vl;
+    KeyLoads<kKeys, kPe / 4> pl;
+    kl.init(kv_at, 4 * kv_row, [&](int r, int c) { return piece(k_first + r, c); });
+    pl.init((const char*)(pe + (long)(keys.begin + k_first) * a.pe_stride), 4 * a.pe_stride,
+            [&](int r, int c) { return piece(k_first + r, c); });
+    vl.init(kv_at + 4 * DV, 4 * kv_row, [](int, int c) { return c; });
     const auto address = [&](float* p) { return (uint32_t)uniform((int)(uint32_t)(uintptr_t)(lds_void*)p); };
-    auto fetch = [&](int buf, int pos) {
-        const int have = keys.end - (pos + wave * kKeys);
-        kl.issue(address(lds.k + (buf * KT + wave * kKeys) * DK), have, kKeys, KT);
-        vl.issue(address(lds.v + (buf * KT + wave * kKeys) * DV), have, kKeys, KT);
+    const auto fetch = [&](int buf, int pos) {
+        const int have = keys.end - (pos + k_first);
+        kl.issue(address(lds.k + (buf * KT + k_first) * DV), have, KT);
+        pl.issue(address(lds.pe + (buf * KT + k_first) * kPe), have, KT);
+        vl.issue(address(lds.v + (buf * KT + k_first) * DV), have, KT);
     };
 
     if (keys.begin < keys.end) fetch(0, keys.begin);
@@ -327,7 +316,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_expanded_f32(ExpandedArg
         __builtin_amdgcn_s_waitcnt(0x0f70);
         __syncthreads();
         if (pos + KT < keys.end) fetch(buf ^ 1, pos + KT);
-        const float* kt = lds.k + buf * KT * DK;
+        const float *kt = lds.k + buf * KT * DV, *pt = lds.pe + buf * KT * kPe;
         float* vt = lds.v + buf * KT * DV;
         bool odd = false;
         if (pos + KT > keys.all) {
@@ -351,7 +340,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_expanded_f32(ExpandedArg
         f32x4 st = zero4();
 #pragma unroll
         for (int i = 0; i < KQ; ++i) {
-            const f32x4 kf = *(const f32x4*)(kt + c16 * DK + 4 * piece(c16, g4 * KQ + i));
+            // (the last lane quarters' channels are partly of the shared part)
+            const int c = g4 * KQ + i;
+            const float* k = c < DV / 4 ? kt + c16 * DV + 4 * piece(c16, c) : pt + c16 * kPe + 4 * piece(c16, c - DV / 4);
+            const f32x4 kf = *(const f32x4*)k;
             for (int j = 0; j < 4; ++j) st = mma4(kf[j], qf[i][j], st);
         }
         for (int i = 0; i < 4; ++i) {

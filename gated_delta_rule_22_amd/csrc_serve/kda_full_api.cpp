@@ -159,6 +159,9 @@ kda_status kda_attn_latent(const void* q, const void* cache, const int* block_ta
     return done(kda::launch_attn_latent(a, ws, (hipStream_t)stream));
 }
 
+// Channels of one key of kda_attn_expanded, or between two shared parts.
+static constexpr int kMaxKeyRow = 1 << 26;
+
 size_t kda_attn_expanded_workspace_size(int T, int B, int H, int dn, int dr, int dv, int max_q,
                                         kda_dtype dtype) {
     if (T <= 0 || B <= 0 || H <= 0 || max_q < 0) return 0;
@@ -177,6 +180,8 @@ kda_status kda_attn_expanded(const void* q, const void* kv, const void* k_pe, co
     if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_UNSUPPORTED;
     if (dr != kda::kPe || dn != dv || (dv != 64 && dv != 128)) return KDA_ERR_UNSUPPORTED;
     if (pe_stride < dr || pe_stride % 8) return KDA_ERR_INVALID_ARG;
+    // (the kernels' offsets over eight keys have 32 bits)
+    if (pe_stride > kMaxKeyRow || product(H, (size_t)dn + dv) > (size_t)kMaxKeyRow) return KDA_ERR_INVALID_ARG;
     if (T == 0 || B == 0 || H == 0) return KDA_OK;
     const size_t elt = dtype == KDA_BF16 ? 2 : 4;
     const size_t rows = product(T, H, (size_t)dn + dr, elt), outs = product(T, H, dv, elt);

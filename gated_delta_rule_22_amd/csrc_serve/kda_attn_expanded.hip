@@ -164,10 +164,10 @@ __global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, 2) void attn_expand
         float mx = -INFINITY;
         for (int u = 0; u < 2; ++u)
             for (int i = 0; i < 16; ++i) mx = fmaxf(mx, st[u][i]);
-        mx = max_halves(mx) * scale;
+        mx *= scale;
         // the reference may stay behind the maximum by up to 8 in the log2 domain
         if (__any(mx > m + 8.f)) {
-            const float mn = fmaxf(m, mx);
+            const float mn = fmaxf(m, max_halves(mx));
             const float c = mn == -INFINITY ? 1.f : exp2_f(m - mn);
             m = mn;
             l *= c;

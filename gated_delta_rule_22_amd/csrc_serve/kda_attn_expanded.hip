@@ -51,14 +51,15 @@ struct KeyLoads {
 
 template <int DV> struct ExpandedShape {
     static constexpr int DK = DV + kPe;
-    static constexpr int kWaves = 8, kRows = 32 * kWaves, KT = 64;
+    static constexpr int kWaves = DV == 64 ? 4 : 8, kRows = 32 * kWaves, KT = 64;
+    static constexpr int kPerSimd = DV == 64 ? 3 : 2;    // waves, by their registers
     static constexpr int kKeys = KT / kWaves;        // that a wave fetches
 };
 
 template <int DV> struct ExpandedLds {
     typedef ExpandedShape<DV> S;
     __align__(128) bf16 k[2 * S::KT * DV], pe[2 * S::KT * kPe], v[2 * S::KT * DV];
-    int odd_wave[S::kWaves];
+    int odd_wave[2][S::kWaves];
     AttnItem item;
 };
 
@@ -68,7 +69,7 @@ template <int D> __device__ __forceinline__ int expanded_piece(int key, int c) {
 }
 
 template <int DV>
-__global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, 2) void attn_expanded_bf16(
+__global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, ExpandedShape<DV>::kPerSimd) void attn_expanded_bf16(
     ExpandedArgs a, AttnSplit s, unsigned first_block) {
     typedef ExpandedShape<DV> S;
     constexpr int DK = S::DK, KT = S::KT, KS = DK / 16, NB = DV / 32, kKeys = S::kKeys;
@@ -87,7 +88,8 @@ __global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, 2) void attn_expand
 
     bf16x8 qf[KS];
     const RowAt at = row_at(a, it, 1, it.tile * s.R + wave * 32 + c32);
-    const int limit = at.in ? (int)min((long)it.kept + at.t, (long)kKeepAll) : INT_MIN;
+    // last of the part's positions that the lane's row sees
+    const int limit = at.in ? (int)min((long)it.kept + at.t, (long)keys.end - 1) : -1;
     // last position that a row of this wave sees
     const int first_row = it.tile * s.R + wave * 32;
     const int wave_limit = first_row < it.n ? uniform((int)min((long)it.kept + first_row + 31, (long)kKeepAll)) : -1;
@@ -120,27 +122,22 @@ __global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, 2) void attn_expand
     int buf = 0;
     for (int pos = keys.begin; pos < keys.end; pos += KT, buf ^= 1) {
         __builtin_amdgcn_s_waitcnt(0x0f70);          // vmcnt(0): this wave's part has landed
-        __syncthreads();
-        if (pos + KT < keys.end) fetch(buf ^ 1, pos + KT);
-        const bf16 *kt = lds.k + buf * KT * DV, *pt = lds.pe + buf * KT * kPe;
-        bf16* vt = lds.v + buf * KT * DV;
-        bool odd = false;
-        if (pos + KT > keys.all) {
-            // Positions that only some rows see: a value there that is not finite must
-            // not meet the weight 0 of the others in a product. It counts 0 here and is
-            // added below for the rows that see it.
+        // Positions that only some rows see: a value there that is not finite must not
+        // meet the weight 0 of the others in a product. The wave that fetched it clears it,
+        // and it is added below for the rows that see it.
+        const bool some = pos + KT > keys.all;
+        if (some) {
+            bool odd = false;
             for (int i = 0; i < LV; ++i) {
-                bf16* v = vt + wave * kKeys * DV + i * 512 + 8 * lane;
+                bf16* v = lds.v + (buf * KT + k_first) * DV + i * 512 + 8 * lane;
                 *(bf16x8*)v = only_finite(*(const bf16x8*)v, odd);
             }
             odd = __any(odd);
-            if (lane == 0) lds.odd_wave[wave] = odd;
-            __syncthreads();                         // the values are cleared, the flags set
-            odd = false;
-            for (int w = 0; w < S::kWaves; ++w) odd |= lds.odd_wave[w] != 0;
-            odd = uniform(odd);
-            __syncthreads();                         // and read
+            if (lane == 0) lds.odd_wave[buf][wave] = odd;
         }
+        __syncthreads();
+        if (pos + KT < keys.end) fetch(buf ^ 1, pos + KT);
+        const bf16 *kt = lds.k + buf * KT * DV, *pt = lds.pe + buf * KT * kPe, *vt = lds.v + buf * KT * DV;
         if (pos > wave_limit) continue;              // no row of this wave sees these keys
         f32x16 st[2];
 #pragma unroll
@@ -154,12 +151,11 @@ __global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, 2) void attn_expand
                 st[u] = mma_big(kf, qf[k], st[u]);
             }
         }
-        if (pos + KT - 1 > limit || pos + KT > keys.end) {
+        if (pos + KT - 1 > limit) {
+            const int seen = limit - pos - 4 * half;
             for (int u = 0; u < 2; ++u)
-                for (int i = 0; i < 16; ++i) {
-                    const int y = 32 * u + 8 * (i / 4) + 4 * half + i % 4;
-                    if (pos + y > limit || pos + y >= keys.end) st[u][i] = -INFINITY;
-                }
+                for (int i = 0; i < 16; ++i)
+                    if (32 * u + 8 * (i / 4) + i % 4 > seen) st[u][i] = -INFINITY;
         }
         float mx = -INFINITY;
         for (int u = 0; u < 2; ++u)
@@ -204,7 +200,9 @@ __global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, 2) void attn_expand
                 acc[b] = mma_big(va, pf[ks], acc[b]);
                 acc[b] = mma_big(va, pr[ks], acc[b]);
             }
-        if (odd) {
+        bool odd = false;
+        for (int w = 0; some && w < S::kWaves; ++w) odd |= lds.odd_wave[buf][w] != 0;
+        if (uniform((int)odd)) {
             // the values left out above, for the rows that see them
             for (int y = 0; y < KT && pos + y < keys.end; ++y) {
                 const bf16* gv = kv + (long)(pos + y) * kv_row + DV;
@@ -258,7 +256,7 @@ __global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, 2) void attn_expand
 template <int DV> struct ExpandedLdsF {
     static constexpr int DK = DV + kPe, KT = 16;
     __align__(128) float k[2 * KT * DV], pe[2 * KT * kPe], v[2 * KT * DV];
-    int odd_wave[4];
+    int odd_wave[2][4];
     AttnItem item;
 };
 constexpr int kRowsF = 64;
@@ -283,7 +281,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_expanded_f32(ExpandedArg
 
     f32x4 qf[KQ];
     const RowAt at = row_at(a, it, 1, it.tile * s.R + wave * 16 + c16);
-    const int limit = at.in ? (int)min((long)it.kept + at.t, (long)kKeepAll) : INT_MIN;
+    const int limit = at.in ? (int)min((long)it.kept + at.t, (long)keys.end - 1) : -1;
     const int wave_limit = uniform((int)min((long)it.kept + it.tile * s.R + wave * 16 + 15, (long)kKeepAll));
     for (int k = 0; k < KQ; ++k) {
         f32x4 z = zero4();
@@ -314,14 +312,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_expanded_f32(ExpandedArg
     int buf = 0;
     for (int pos = keys.begin; pos < keys.end; pos += KT, buf ^= 1) {
         __builtin_amdgcn_s_waitcnt(0x0f70);
-        __syncthreads();
-        if (pos + KT < keys.end) fetch(buf ^ 1, pos + KT);
-        const float *kt = lds.k + buf * KT * DV, *pt = lds.pe + buf * KT * kPe;
-        float* vt = lds.v + buf * KT * DV;
-        bool odd = false;
-        if (pos + KT > keys.all) {
+        const bool some = pos + KT > keys.all;
+        if (some) {
+            bool odd = false;
             for (int i = 0; i < LV; ++i) {
-                f32x4* v = (f32x4*)(vt + wave * kKeys * DV + i * 256 + 4 * lane);
+                f32x4* v = (f32x4*)(lds.v + (buf * KT + k_first) * DV + i * 256 + 4 * lane);
                 f32x4 x = *v;
                 for (int j = 0; j < 4; ++j)
                     if (!finite_bits(x[j])) {
@@ -331,11 +326,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_expanded_f32(ExpandedArg
                 *v = x;
             }
             odd = __any(odd);
-            if (lane == 0) lds.odd_wave[wave] = odd;
-            __syncthreads();
-            odd = uniform(lds.odd_wave[0] | lds.odd_wave[1] | lds.odd_wave[2] | lds.odd_wave[3]);
-            __syncthreads();
+            if (lane == 0) lds.odd_wave[buf][wave] = odd;
         }
+        __syncthreads();
+        if (pos + KT < keys.end) fetch(buf ^ 1, pos + KT);
+        const float *kt = lds.k + buf * KT * DV, *pt = lds.pe + buf * KT * kPe, *vt = lds.v + buf * KT * DV;
         if (pos > wave_limit) continue;
         f32x4 st = zero4();
 #pragma unroll
@@ -348,8 +343,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_expanded_f32(ExpandedArg
         }
         for (int i = 0; i < 4; ++i) {
             st[i] *= scale;
-            const int key = pos + 4 * g4 + i;
-            if (key > limit || key >= keys.end) st[i] = -INFINITY;
+            if (pos + 4 * g4 + i > limit) st[i] = -INFINITY;
         }
         const float mx = max_quarters(fmaxf(fmaxf(st[0], st[1]), fmaxf(st[2], st[3])));
         if (__any(mx > m)) {
@@ -371,7 +365,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_expanded_f32(ExpandedArg
                 const f32x4 x = *(const f32x4*)(vt + (4 * g4 + i) * DV + 64 * g + 4 * c16);
                 for (int j = 0; j < 4; ++j) acc[4 * g + j] = mma4(x[j], st[i], acc[4 * g + j]);
             }
-        if (odd) {
+        bool odd = false;
+        for (int w = 0; some && w < 4; ++w) odd |= lds.odd_wave[buf][w] != 0;
+        if (uniform((int)odd)) {
             for (int y = 0; y < KT && pos + y < keys.end; ++y) {
                 const float* gv = kv + (long)(pos + y) * kv_row + DV;
                 float w = 0.f;
@@ -416,7 +412,7 @@ struct ExpandedPlan {
 };
 ExpandedPlan plan_of(int T, int B, int H, int dv, int max_q, bool bf16_io) {
     ExpandedPlan p{};
-    p.l = launch_of(T, B, 1, H, bf16_io ? 256 : kRowsF, 9, 9, 9, INT32_MAX);
+    p.l = launch_of(T, B, 1, H, bf16_io ? dv == 64 ? ExpandedShape<64>::kRows : ExpandedShape<128>::kRows : kRowsF, 10, 10, 9, INT32_MAX);
     p.bytes = (size_t)p.l.split.slots * p.l.split.R * (dv + 2) * sizeof(float);
     if (B > kBlock) p.bytes += AttnTable::ints(B) * sizeof(int);
     return p;

@@ -412,7 +412,13 @@ struct ExpandedPlan {
 };
 ExpandedPlan plan_of(int T, int B, int H, int dv, int max_q, bool bf16_io) {
     ExpandedPlan p{};
-    p.l = launch_of(T, B, 1, H, bf16_io ? dv == 64 ? ExpandedShape<64>::kRows : ExpandedShape<128>::kRows : kRowsF, 10, 10, 9, INT32_MAX);
+    // Heads of 64 have room for 768 workgroups on the card, and shorter parts of ragged
+    // prompts pay: 64 -> 58 us with up to 2^11 parts, and 2^10 rather than parts shorter
+    // than kLongPart (2^11 of them 63, 2^12 69). Others have room for 256.
+    const bool small = bf16_io && dv == 64;
+    const int rows = !bf16_io ? kRowsF : small ? ExpandedShape<64>::kRows : ExpandedShape<128>::kRows;
+    const int most = small ? 11 : 9, few = small ? 10 : 9;
+    p.l = launch_of(T, B, 1, H, rows, most, most, few, INT32_MAX);
     p.bytes = (size_t)p.l.split.slots * p.l.split.R * (dv + 2) * sizeof(float);
     if (B > kBlock) p.bytes += AttnTable::ints(B) * sizeof(int);
     return p;

@@ -36,16 +36,6 @@ __device__ __forceinline__ long token_position(const int* cu, const int* kept, i
 template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
 template <typename T> using Vec = T __attribute__((ext_vector_type(16 / sizeof(T))));
 
-template <bool NT, typename V>
-__device__ __forceinline__ V load_vec(const V* p) {
-    return NT ? __builtin_nontemporal_load(p) : *p;
-}
-template <bool NT, typename V>
-__device__ __forceinline__ void store_vec(V* p, V x) {
-    if (NT) __builtin_nontemporal_store(x, p);
-    else *p = x;
-}
-
 // cos and sin of the token's pairs, in the wave's own part of LDS. Angles and
 // their functions are fp64: at a position of 2^20 an fp32 angle of the fastest
 // pair is off by 2^-5. They cost nothing where a wave has 16 rows or more to

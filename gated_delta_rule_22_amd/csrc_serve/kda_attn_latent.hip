@@ -2,16 +2,25 @@
 // key of all query heads, and c its value. Online softmax as in the paged
 // attention of grouped heads (kda_attn_paged.hip).
 //
-// A request's rows are its new tokens times all query heads, cut into tiles of
-// 32 RT rows; a workgroup of four waves takes a tile and a part of its keys
-// (kda_attn_sched.h). The keys go through LDS, KT at a time, where they serve as
-// keys and as values. The waves divide a step's work twice:
-//   scores  wave w takes 32 rows (their queries stay in its registers) and a
-//           quarter, half or all of the step's keys, S^T = K Q^T;
-//   values  each wave takes a quarter of the value channels for all rows,
-//           O^T += V^T P^T, so that V is read from LDS once, not by every wave.
-// The weights P pass through LDS in between, in the order of the second product's
-// operand.
+// A request's rows are its new tokens times all query heads, cut into tiles of R = 32 or
+// 64 rows. The call's tiles times keys are shared out evenly between as many workgroups
+// as the card holds (kda_attn_even.h): parts of whole tiles left compute units idle for a
+// third to a half of the time, since a tile has few rows and a long request many keys.
+// The keys go through LDS 32 at a time, where they serve as keys and as values.
+//
+// bf16 weights are two terms, a leading part and its rest, so that only the result is
+// rounded: 2^-16 of a weight is lost. Per row and key 2 (dc + 64) + 4 dc flops.
+//
+// What bounds it, and what it measured with 512 + 64 channels:
+//   256 single tokens, 16 heads, 2.7 GB of cache: 526 us, 5.1 TB/s, the memory's rate;
+//   128 single tokens, 128 heads, 199 GF: 355 us. Each 64 rows of a request read its keys
+//     again, from the last-level cache if they do it at the same time (`side`);
+//   4 drafts of 8 tokens over up to 262144 keys, 32 heads, 353 GF: 510 us, 690 TF/s, and
+//     1020 with the weights' second terms;
+//   one token over 1000 keys, 32 heads: 21 us, of which two launches are 10, and the rest
+//     one chain of memory latencies: lengths, pages, queries and keys, pieces.
+// 64 rows need 256 registers a lane with 512 channels. Some of them are spilled outside of
+// the products' loops; tiles of 128 rows spill in them (390 -> 700 us).
 #include "kda_attn_even.h"
 #include "kda_full_launch.h"
 
@@ -198,9 +207,10 @@ struct KeySteps {
 // Tiles of 32 and 64 rows: waves 0 to 3 make the weights, waves 4 to 7 the values of
 // the step before, so that each SIMD has one of both and a step has one barrier. Score
 // wave rg + 2 kg has half of the rows and 16 keys. The rows' reference is what all
-// their keys' maxima were up to the step before: a weight may be up to 2^60 then, which
-// costs nothing in fp32 and bf16. Where a maximum jumps further (the first step of a
-// run, for one), the step's weights are made again behind the barrier.
+// their keys' maxima were up to the step before: a weight may be up to 2^24 then, which
+// costs nothing in fp32 and bf16 (and values up to 2^103 do not overflow with it). Where a
+// maximum jumps further (the first step of a run, for one), the step's weights are made
+// again behind the barrier.
 template <int DC, int R> struct NarrowLds {
     static constexpr int W = DC + kPe, RP = R / 16;
     static constexpr int BUF = R == 64 && DC == 512 ? 3 : 4;     // what LDS holds
@@ -211,7 +221,7 @@ template <int DC, int R> struct NarrowLds {
     int moved[2][2], odd[32];
     EvenItem item;
 };
-constexpr float kJump = 60.f;
+constexpr float kJump = 24.f;
 
 template <int DC, int R>
 __device__ __forceinline__ void narrow_run(const AttnArgs& a, const EvenSplit& e, const EvenRun& it,

@@ -153,6 +153,7 @@ __device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, const voi
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  ::"s"(to), "v"(off), "s"(base) : "memory", "m0");
 }
+
 // The lists of a call of many requests (AttnTable), a workgroup for each of
 // its launches: sixteen waves sum the work and then the parts of their blocks,
 // the first one puts the blocks' sums in order. 4096 requests of one token over
@@ -365,10 +366,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(A a, AttnSplit s0, Att
         }
     }
 }
+
 struct Launch {
     AttnSplit split;
     long items, joins;     // workgroups
-};Launch launch_of(long T, long B, long G, long Hkv, int R, int most_log2, int some_log2,
+};
+Launch launch_of(long T, long B, long G, long Hkv, int R, int most_log2, int some_log2,
                  int few_log2, int max_rows) {
     Launch l{};
     l.split.R = R;
@@ -389,7 +392,9 @@ struct Launch {
     const long rows = (tiles < target ? tiles : target) * R;
     l.joins = rows < 1024 ? rows : 1024;
     return l;
-}// Workgroups of a launch: a grid holds fewer than 2^32 threads, and the calls
+}
+
+// Workgroups of a launch: a grid holds fewer than 2^32 threads, and the calls
 // that are accepted make up to 2^31 parts (one each for T Hq of 2^30).
 constexpr unsigned kGrid = 1u << 23;
 template <typename F>

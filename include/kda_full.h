@@ -133,7 +133,8 @@ kda_status kda_attn_latent(const void* q, const void* cache, const int* block_ta
  *            kernels only
  *   scale    0 selects 1 / sqrt(dn + dr). Not negative, at most 2^127.
  * Masked positions do not reach the result, whatever they hold. dr = 64,
- * dn = dv in {64, 128}; T * H, N and B are at most 2^30.
+ * dn = dv in {64, 128}; T * H, N and B are at most 2^30, H (dn + dv) and pe_stride at
+ * most 2^26.
  */
 size_t kda_attn_expanded_workspace_size(int T, int B, int H, int dn, int dr, int dv, int max_q,
                                         kda_dtype dtype);

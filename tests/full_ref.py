@@ -157,6 +157,16 @@ def expanded(c):
     return o, lse, spread, mag
 
 
+def jumps(total, seed):
+    """What a position adds to its scores, in the log2 domain: nothing at most of them,
+    and peaks of all sizes at some, so that a running maximum jumps by little and much."""
+    g = torch.Generator().manual_seed(seed)
+    kind = torch.randint(0, 40, (total,), generator=g)
+    size = torch.tensor([5.0, 9.0, 20.0, 23.0, 26.0, 40.0, 70.0, 130.0, -30.0, -200.0])
+    x = torch.where(kind < 10, size[kind.clamp(max=9)], torch.zeros(total))
+    return x * torch.linspace(0.1, 1.0, total)
+
+
 def before_rounding(spread, mag, width, keys, dtype):
     """Largest error of a result before it is rounded to its type.
 
@@ -164,7 +174,7 @@ def before_rounding(spread, mag, width, keys, dtype):
     mag; it enters the weights through exp (v_exp_f32: 2^-22 relative, and the
     rounding of its argument, of size at most 2 mag log2 e: 2^-23 mag), which moves
     numerator and denominator: factor 2. A row's weights are relative to a reference
-    that may be off its maximum by 2^8, which costs nothing in fp32. Sums over the
+    that may be off its maximum by 2^24, which costs nothing in fp32. Sums over the
     keys: one step a key in the weights' sum and one (bf16: two) in the values', each
     of which may lose 2^-23 where a product is cut off instead of rounded; the joins
     add fewer than 128. bf16: a weight in two bf16 terms lacks 2^-15 of itself (the

@@ -178,6 +178,13 @@ def attn_expanded(lib, **kw):
 
 
 @no_gpu
+def test_attn_expanded_rejects_keys_too_wide(lib):
+    assert attn_expanded(lib, N=1, ld=(1 << 26) + 8) == INVALID
+    assert attn_expanded(lib, T=1, N=1, H=(1 << 18) + 1) == INVALID
+    assert attn_expanded(lib, T=1, N=1, H=(1 << 19) + 1, dn=64, dv=64) == INVALID
+
+
+@no_gpu
 def test_attn_expanded_rejects(lib):
     for name in ("T", "N", "B", "H", "max_q"):
         assert attn_expanded(lib, **{name: -1}) == INVALID, name

@@ -184,6 +184,42 @@ def test_long_contexts_in_parts(n, keys, H, dn, dtype):
     assert rel <= (2.0 ** -10 if dtype == BF else 2.0 ** -15), rel
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,keys,H,dn", [([1, 40], [900, 300], 5, 64), ([300, 7], [700, 2000], 3, 128)])
+def test_maxima_that_jump(n, keys, H, dn, dtype):
+    c = R.expanded_case(n, keys, H, dn, dtype, seed=70)
+    T = c["cu"][-1]
+    rows = torch.arange(T * H).view(T, H) % 5
+    c["q"][:T, :, dn + 1] = torch.tensor([0.0, 1.0, 0.5, -1.0, 0.03125])[rows].to(dtype)
+    for i, total in enumerate(keys):
+        c["pe_all"][c["ck"][i]:c["ck"][i + 1], -63] = (R.jumps(total, 70 + i) / (c["scale"] * 1.4427)).to(dtype)
+    check(c)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dn", [64, 128])
+def test_workspace_of_the_named_size(dn, dtype):
+    c = R.expanded_case([300, 1, 40], [1300, 700, 40], 5, dn, dtype, seed=72)
+    need = kda.kda_attn_expanded_workspace_size(341, 3, 5, dn, 64, dn, 300, dtype)
+    ws = torch.full((need + 4096,), 0xAB, dtype=torch.uint8, device=DEV)
+    check(c, max_q=300, workspace=ws)
+    assert bool((ws[need:] == 0xAB).all())
+    check(c, max_q=300, workspace=ws[:need - 1])          # too small: another one is used
+
+
+def test_widest_keys():
+    # rows of keys and the shared part's stride have a limit
+    c = R.expanded_case([2], [3], 1, 64, BF, seed=73)
+    q, kv, pe, cu, ck = tensors(c)
+    wide = torch.zeros(2 * (1 << 26) + 64 + 128, dtype=BF, device=DEV)
+    at = wide.as_strided((3, 64), (1 << 26, 1))
+    at.copy_(pe)
+    o = kda.kda_attn_expanded(q, kv, at, cu, ck, dv=64, want_lse=True)
+    verdict(c, o[0].cpu(), o[1].cpu(), R.expanded(c))
+    with pytest.raises(kda.KDAError):
+        kda.kda_attn_expanded(q, kv, wide.as_strided((3, 64), ((1 << 26) + 8, 1)), cu, ck, dv=64)
+
+
 @pytest.mark.parametrize("n", [1, 400])
 def test_identical_calls_streams_and_graphs(n):
     c = R.expanded_case([n, 30], [3000, 400], 4, 128, BF, seed=50)

@@ -90,6 +90,50 @@ def test_rising_and_falling_scores(Hq, n, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("big", [0, 90])
+@pytest.mark.parametrize("Hq,n,dc", [(3, 1, 128), (16, 2, 512), (40, 1, 512), (20, 5, 256), (7, 40, 128)])
+def test_maxima_that_jump(Hq, n, dc, big, dtype):
+    # peaks anywhere, for all rows, for some or for none; with values of 2^90, which a
+    # weight far above 1 must not carry out of fp32
+    c = R.latent_case([n, n, 1], [900, 333, 2100], Hq, dc, 16, dtype, seed=70)
+    T = c["cu"][-1]
+    rows = torch.arange(T * Hq).view(T, Hq) % 5
+    c["q"][:T, :, dc + 1] = torch.tensor([0.0, 1.0, 0.5, -1.0, 0.03125])[rows].to(dtype)
+    if big:
+        c["q"][:T, :, :dc] = 0.0
+    for i, total in enumerate((900 + n, 333 + n, 2101)):
+        x = R.jumps(total, 70 + i) / (c["scale"] * 1.4427)
+        pages = c["table"][i, torch.arange(total) // 16].long()
+        c["cache"][pages, torch.arange(total) % 16, dc + 1] = x.to(dtype)
+        c["cache"][pages, torch.arange(total) % 16, :dc] *= 2.0 ** big
+    check(c)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Hq,n,ctx,hint", [
+    (128, [1] * 6, [0, 1, 700, 63, 3000, 64], 1),          # two tiles of 64 rows, or four of 32
+    (64, [4, 4, 4], [5, 2000, 90], 4),                     # four
+    (64, [1, 7, 0], [900, 33, 5], 4),                      # the hint's product is T, no length is
+    (96, [2, 2], [40, 1500], 2),                           # three of 64, six of 32
+    (128, [1], [0], 1), (128, [1], [9], 1),                # fewer units than workgroups
+    (64, [1] * 300, [(37 * i) % 150 for i in range(300)], 1)])
+def test_rows_of_equal_requests_side_by_side(Hq, n, ctx, hint, dtype):
+    c = R.latent_case(n, ctx, Hq, 512 if len(n) < 9 else 128, 64, dtype, seed=71)
+    check(c, max_new=hint)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Hq,n", [(16, 1), (128, 1), (9, 30)])
+def test_workspace_of_the_named_size(Hq, n, dtype):
+    c = R.latent_case([n] * 3, [1500, 40, 7], Hq, 256, 32, dtype, seed=72)
+    need = kda.kda_attn_latent_workspace_size(3 * n, 3, Hq, 256, 64, n, dtype)
+    ws = torch.full((need + 4096,), 0xAB, dtype=torch.uint8, device=DEV)
+    check(c, max_new=n, workspace=ws)
+    assert bool((ws[need:] == 0xAB).all())
+    check(c, max_new=n, workspace=ws[:need - 1])          # too small: another one is used
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("Hq,n,ctx", [(2, 8, 3), (8, 20, 70), (50, 3, 40), (16, 8, 300)])
 @pytest.mark.parametrize("what", [float("inf"), float("-inf"), float("nan")])
 def test_masked_positions_stay_out(Hq, n, ctx, what, dtype):

@@ -241,8 +241,8 @@ def kda_attn_expanded(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_
         _kda._check(k_pe, "k_pe", (N, dr), dt, dev)
     # (of a single row, or of none, the stride means nothing)
     stride_pe, column = k_pe.stride() if N > 1 else (dr, k_pe.stride(1))
-    if column != 1 or stride_pe < dr or stride_pe % 8:
-        raise ValueError("k_pe's rows must be contiguous, a multiple of 8 elements apart")
+    if column != 1 or stride_pe < dr or stride_pe % 8 or stride_pe > 1 << 26:
+        raise ValueError("k_pe's rows must be contiguous, a multiple of 8 and at most 2^26 elements apart")
     i32 = torch.int32
     o = _out(o, (T, H, dv), dt, dev, stream)
     if lse is None and want_lse:

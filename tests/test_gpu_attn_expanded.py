@@ -216,8 +216,10 @@ def test_widest_keys():
     at.copy_(pe)
     o = kda.kda_attn_expanded(q, kv, at, cu, ck, dv=64, want_lse=True)
     verdict(c, o[0].cpu(), o[1].cpu(), R.expanded(c))
-    with pytest.raises(kda.KDAError):
-        kda.kda_attn_expanded(q, kv, wide.as_strided((3, 64), ((1 << 26) + 8, 1)), cu, ck, dv=64)
+    wide = torch.empty((1 << 33) + 192, dtype=BF, device=DEV)    # 32 bits would cut strides to 0 and 64
+    for stride in ((1 << 26) + 8, 1 << 32, (1 << 32) + 64):
+        with pytest.raises(ValueError):
+            kda.kda_attn_expanded(q, kv, wide.as_strided((3, 64), (stride, 1)), cu, ck, dv=64)
 
 
 @pytest.mark.parametrize("n", [1, 400])

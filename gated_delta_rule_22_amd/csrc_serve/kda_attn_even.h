@@ -17,6 +17,8 @@
 // tile to it.
 #pragma once
 
+#include <type_traits>
+
 #include "kda_attn_rows.h"
 
 namespace kda {
@@ -354,6 +356,32 @@ __global__ __launch_bounds__(kAttnThreads) void even_join(A a, EvenSplit e) {
             for (int i = 0; i < 4; ++i) o[i] = from_f32<T>(y.v[i] * inv);
             if (a.lse && d == 0) a.lse[to.q] = y.l == 0.f ? -INFINITY : (y.m + __log2f(y.l)) * kLn2;
         };
+        // N pieces of each of M rows in flight
+        const auto few = [&](auto n, auto m) {
+            constexpr int N = decltype(n)::value, M = decltype(m)::value;
+            for (int row = group; row < have; row += M * kGroups) {
+                Joined z[M][N];
+#pragma unroll
+                for (int r = 0; r < M; ++r)
+#pragma unroll
+                    for (int p = 0; p < N; ++p) z[r][p] = part(row_a + min(row + r * kGroups, have - 1), p);
+#pragma unroll
+                for (int r = 0; r < M; ++r) {
+                    Joined y;
+#pragma unroll
+                    for (int p = 0; p < N; ++p) y.add(z[r][p]);
+                    if (row + r * kGroups < have) write(y, row_a + row + r * kGroups);
+                }
+            }
+        };
+        if (pieces <= 2) {
+            few(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
+            continue;
+        }
+        if (pieces <= 4) {
+            few(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+            continue;
+        }
         if (pieces <= 16) {                          // eight pieces in flight
             for (int row = group; row < have; row += kGroups) {
                 Joined y;

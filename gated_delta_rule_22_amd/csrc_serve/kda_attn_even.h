@@ -102,8 +102,12 @@ __device__ __forceinline__ int even_begin(const EvenSplit& e, int total, int w) 
     return w < G ? (int)((long)w * total / G) : total;
 }
 
-// Unit y of the call, or workgroup w's first one (y < 0), into LDS; by one wave.
-// found = false: there is none.
+// The runs from unit y of the call, or workgroup w's first one (y < 0), up to that
+// workgroup's last unit, into LDS; by one wave. found = false: there are no more. Several
+// at once, for each alone would wait for the lengths again (a call of more than kBlock
+// requests: one, the others may be in other blocks).
+constexpr int kEvenRuns = 4;
+__device__ __forceinline__ int even_at_once(const EvenSplit& e) { return e.table ? 1 : kEvenRuns; }
 template <typename A>
 __device__ __forceinline__ void even_find(const A& a, const AttnSplit& s, const EvenSplit& e, int y, int w,
                                           EvenItem* to) {
@@ -137,11 +141,17 @@ __device__ __forceinline__ void even_find(const A& a, const AttnSplit& s, const 
         if (__any(block.back()) && wave_total(block.claims()) > a.T) total = 0;
         if (y < 0) y = even_begin(e, total, w);
     }
-    if (lane == 0) {
-        to->found = false;
-        to->total = total;
+    const int y1 = even_begin(e, total, w + 1);
+    for (int k = 0; k < even_at_once(e); ++k) {
+        if (lane == 0) {
+            to[k].found = false;
+            to[k].total = total;
+        }
+        if (y >= y1) continue;
+        block.find_even(base, y - before, C, to + k);
+        lds_fence_wave();
+        y += min(uniform(to[k].units) - uniform(to[k].unit), y1 - y);
     }
-    if (y < total) block.find_even(base, y - before, C, to);
 }
 
 // What a workgroup has of a tile.
@@ -196,37 +206,40 @@ __device__ __forceinline__ RowAt run_row(const AttnArgs& a, const EvenRun& it, i
 
 // A workgroup's runs in turn, each with what is left in LDS free to use.
 template <typename A, typename F>
-__device__ __forceinline__ void even_runs(const A& a, const AttnSplit& s, const EvenSplit& e, EvenItem& item, F run) {
+__device__ __forceinline__ void even_runs(const A& a, const AttnSplit& s, const EvenSplit& e, EvenItem* items, F run) {
     // workgroups go to the 8 XCDs in turn: neighbours in the units on the same one
     const int n = gridDim.x, b = blockIdx.x, v = n % 8 ? b : b % 8 * (n / 8) + b / 8;
     const int w = v / e.side, side = v - w * e.side;
     int y = -1, y1 = 0;
     for (;;) {
-        if (wave_id() == 0) even_find(a, s, e, y, w, &item);
+        if (wave_id() == 0) even_find(a, s, e, y, w, items);
         __syncthreads();
-        const bool first = y < 0;
-        if (first) {
-            const int total = uniform(item.total);
-            y = even_begin(e, total, w);
-            y1 = even_begin(e, total, w + 1);
+        for (int k = 0; k < even_at_once(e); ++k) {
+            const EvenItem& item = items[k];
+            const bool first = y < 0;
+            if (first) {
+                const int total = uniform(item.total);
+                y = even_begin(e, total, w);
+                y1 = even_begin(e, total, w + 1);
+            }
+            const bool more = y < y1 && uniform((int)item.found) != 0;
+            EvenRun it{};
+            if (more) it = even_run(item, e, w, y, y1);
+            it.tile = it.tile * e.side + side;
+            it.slot += 2 * v;
+            const bool rows = it.tile * e.R < it.n * a.Hq;
+            if (first && threadIdx.x == 0) {
+                int* x = e.pieces + 4 * v;
+                x[0] = it.row0;
+                x[1] = it.tile;
+                x[2] = it.n;
+                x[3] = more && rows && it.piece == 1 ? it.pieces : 0;
+            }
+            if (!more) return;
+            y += it.units;
+            if (it.piece >= 0 && rows) run(it);
+            __syncthreads();                         // the run's last reads of LDS are done
         }
-        bool more = y < y1 && uniform((int)item.found) != 0;
-        EvenRun it{};
-        if (more) it = even_run(item, e, w, y, y1);
-        it.tile = it.tile * e.side + side;
-        it.slot += 2 * v;
-        const bool rows = it.tile * e.R < it.n * a.Hq;
-        if (first && threadIdx.x == 0) {
-            int* x = e.pieces + 4 * v;
-            x[0] = it.row0;
-            x[1] = it.tile;
-            x[2] = it.n;
-            x[3] = more && rows && it.piece == 1 ? it.pieces : 0;
-        }
-        if (!more) return;
-        y += it.units;
-        if (it.piece >= 0 && rows) run(it);
-        __syncthreads();                             // the run's last reads of LDS are done
     }
 }
 

@@ -219,7 +219,7 @@ template <int DC, int R> struct NarrowLds {
     float top[2][2][R], factor[2][R], sum[2][R], ref[R];
     __align__(16) int jump[2][4];
     int moved[2][2], odd[32];
-    EvenItem item;
+    EvenItem items[kEvenRuns];
 };
 constexpr float kJump = 24.f;
 
@@ -502,7 +502,7 @@ __device__ __forceinline__ void narrow_run(const AttnArgs& a, const EvenSplit& e
 template <int DC, int R>
 __global__ __launch_bounds__(kLatentThreads, 2) void attn_latent_narrow(AttnArgs a, AttnSplit s, EvenSplit e) {
     __shared__ NarrowLds<DC, R> lds;
-    even_runs(a, s, e, lds.item, [&](const EvenRun& it) { narrow_run<DC, R>(a, e, it, lds); });
+    even_runs(a, s, e, lds.items, [&](const EvenRun& it) { narrow_run<DC, R>(a, e, it, lds); });
 }
 
 // fp32: 32 rows, 32 keys a step. Scores: a wave takes 16 rows and 16 keys, lane
@@ -515,7 +515,7 @@ template <int DC> struct LatentLdsF {
     __align__(16) float p[2 * 2 * 64 * 4];
     float top[2][32], factor[32], sum[2][32];
     int moved[2], odd[KT];
-    EvenItem item;
+    EvenItem items[kEvenRuns];
 };
 constexpr int kRowsF = 32;
 
@@ -692,7 +692,7 @@ __device__ __forceinline__ void latent_run_f32(const AttnArgs& a, const EvenSpli
 template <int DC>
 __global__ __launch_bounds__(kAttnThreads, 1) void attn_latent_f32(AttnArgs a, AttnSplit s, EvenSplit e) {
     __shared__ LatentLdsF<DC> lds;
-    even_runs(a, s, e, lds.item, [&](const EvenRun& it) { latent_run_f32<DC>(a, e, it, lds); });
+    even_runs(a, s, e, lds.items, [&](const EvenRun& it) { latent_run_f32<DC>(a, e, it, lds); });
 }
 
 // Kernel and work split of a call, from sizes alone.

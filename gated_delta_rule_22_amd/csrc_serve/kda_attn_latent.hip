@@ -12,12 +12,12 @@
 // rounded: 2^-16 of a weight is lost. Per row and key 2 (dc + 64) + 4 dc flops.
 //
 // What bounds it, and what it measured with 512 + 64 channels:
-//   256 single tokens, 16 heads, 2.7 GB of cache: 526 us, 5.1 TB/s, the memory's rate;
-//   128 single tokens, 128 heads, 199 GF: 355 us. Each 64 rows of a request read its keys
+//   256 single tokens, 16 heads, 2.7 GB of cache: 495 us, 5.5 TB/s, the memory's rate;
+//   128 single tokens, 128 heads, 199 GF: 335 us. Each 64 rows of a request read its keys
 //     again, from the last-level cache if they do it at the same time (`side`);
-//   4 drafts of 8 tokens over up to 262144 keys, 32 heads, 353 GF: 510 us, 690 TF/s, and
-//     1020 with the weights' second terms;
-//   one token over 1000 keys, 32 heads: 21 us, of which two launches are 10, and the rest
+//   4 drafts of 8 tokens over up to 262144 keys, 32 heads, 353 GF: 490 us, 720 TF/s, and
+//     1060 with the weights' second terms;
+//   one token over 1000 keys, 32 heads: 20.5 us, of which two launches are 10, and the rest
 //     one chain of memory latencies: lengths, pages, queries and keys, pieces.
 // 64 rows need 256 registers a lane with 512 channels. Some of them are spilled outside of
 // the products' loops; tiles of 128 rows spill in them (390 -> 700 us).

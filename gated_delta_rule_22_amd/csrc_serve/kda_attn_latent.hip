@@ -206,11 +206,13 @@ struct KeySteps {
 
 // Tiles of 32 and 64 rows: waves 0 to 3 make the weights, waves 4 to 7 the values of
 // the step before, so that each SIMD has one of both and a step has one barrier. Score
-// wave rg + 2 kg has half of the rows and 16 keys. The rows' reference is what all
-// their keys' maxima were up to the step before: a weight may be up to 2^24 then, which
-// costs nothing in fp32 and bf16 (and values up to 2^103 do not overflow with it). Where a
-// maximum jumps further (the first step of a run, for one), the step's weights are made
-// again behind the barrier.
+// wave rg + 2 kg has half of the rows and 16 keys. The rows' reference is their maximum
+// up to the step before, or less than that by up to kFollow. Where a step's maximum is
+// above it by more than kJump (in the first step of a run, for one), the step's weights
+// are made again behind the barrier. So a weight is at most 2^8, as in the other
+// attention kernels: it costs nothing in fp32 and bf16, and the sums of n keys stay
+// inside fp32 with values up to 2^119 / n. (Following from 8 on and making weights again
+// from 24 on took as long: 16 heads 479 us, 128 heads 332 to 336, drafts 500 to 510.)
 template <int DC, int R> struct NarrowLds {
     static constexpr int W = DC + kPe, RP = R / 16;
     static constexpr int BUF = R == 64 && DC == 512 ? 3 : 4;     // what LDS holds
@@ -221,7 +223,7 @@ template <int DC, int R> struct NarrowLds {
     int moved[2][2], odd[32];
     EvenItem items[kEvenRuns];
 };
-constexpr float kJump = 24.f;
+constexpr float kFollow = 4.f, kJump = 8.f;      // log2
 
 template <int DC, int R>
 __device__ __forceinline__ void narrow_run(const AttnArgs& a, const EvenSplit& e, const EvenRun& it,
@@ -343,13 +345,13 @@ __device__ __forceinline__ void narrow_run(const AttnArgs& a, const EvenSplit& e
                 for (int i = 0; i < kAhead; ++i) kf[i] = read(i);
             }
             if (j == steps) break;
-            // The reference may stay behind the maximum by up to 8 in the log2 domain.
+            // The reference may stay behind the maximum by up to kFollow.
             bool ahead = false;
 #pragma unroll
             for (int rt = 0; rt < RTW; ++rt) {
                 factor[rt] = 1.f;
                 if (j == 0) top[rt] = -INFINITY;
-                ahead |= top[rt] > m[rt] + 8.f;
+                ahead |= top[rt] > m[rt] + kFollow;
             }
             const bool moved = __any(ahead);
             if (moved) {

@@ -51,8 +51,11 @@ __global__ __launch_bounds__(64 * kRopeWaves) void latent_append_kernel(LatentAp
         q = *(const Vt*)(from + a.dc + unit.b);
         unit.apply(p, q);
     }
+    // The factor is inv 2^e, for one of rows of 1e-39 or 1e38 (eps 0) is no normal fp32
+    // number. (Products in fp64 instead: 67.3 us, not 65.9, with 21414 tokens in bf16.)
     float inv = 1.f;
-    if (a.normalise) inv = (float)(1.0 / sqrt(wave_sum(sum) / a.dc + (double)a.eps));
+    int e = 0;
+    if (a.normalise) inv = (float)frexp(1.0 / sqrt(wave_sum(sum) / a.dc + (double)a.eps), &e);
 #pragma unroll
     for (int i = 0; i < kMost; ++i) {
         const int c = (i * 64 + lane) * V;
@@ -60,7 +63,7 @@ __global__ __launch_bounds__(64 * kRopeWaves) void latent_append_kernel(LatentAp
         if (a.normalise)
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                x[i][j] = from_f32<T>(to_f32(x[i][j]) * inv * (a.w ? a.w[c + j] : 1.f));
+                x[i][j] = from_f32<T>(ldexpf(to_f32(x[i][j]), e) * inv * (a.w ? a.w[c + j] : 1.f));
         if (to) *(Vt*)(to + c) = x[i];
         if (out) *(Vt*)(out + c) = x[i];
     }

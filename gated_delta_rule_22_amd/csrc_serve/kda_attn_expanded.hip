@@ -228,7 +228,8 @@ __global__ __launch_bounds__(64 * ExpandedShape<DV>::kWaves, ExpandedShape<DV>::
         }
     }
 
-    const float sum = l + __shfl_xor(l, 32);
+    // (a score past fp32, whose difference to the infinite maximum gave the weight 0)
+    const float sum = m == INFINITY ? NAN : l + __shfl_xor(l, 32);
     const int row = wave * 32 + c32;
     if (it.parts > 1) {
         const long slot = (long)it.slot + ((long)it.part * it.tiles + it.tile) * a.Hkv + it.h;

@@ -103,7 +103,8 @@ kda_status kda_latent_append(const void* kv, const float* w, const int* slot_map
  *   scale    above 0, at most 2^127: 1 / sqrt(width of the queries before they
  *            absorbed anything)
  * Sums over positions are fp32, of weights up to 2^8: |c| times the number of
- * positions that a row sees is meant to be at most 2^118.
+ * positions that a row sees is meant to be at most 2^118. Scores (times log2 e) that
+ * are past fp32 count as infinite.
  * What masked positions and unused cache rows hold does not reach the result; a
  * row that sees a position that is not finite is not finite, in part or as a
  * whole. dr = 64, dc in {128, 256, 512}; T * Hq, max_pages * page_size and B are
@@ -135,7 +136,8 @@ kda_status kda_attn_latent(const void* q, const void* cache, const int* block_ta
  *            kernels only
  *   scale    0 selects 1 / sqrt(dn + dr). Not negative, at most 2^127.
  * Masked positions do not reach the result, whatever they hold. Values are meant to
- * be at most 2^118 over the number of keys, as in kda_attn_latent. dr = 64,
+ * be at most 2^118 over the number of keys, and scores that are past fp32 count as
+ * infinite, as in kda_attn_latent. dr = 64,
  * dn = dv in {64, 128}; T * H, N and B are at most 2^30, H (dn + dv) and pe_stride at
  * most 2^26.
  */

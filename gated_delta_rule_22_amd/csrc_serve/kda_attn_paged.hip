@@ -730,7 +730,8 @@ __device__ __forceinline__ void tile_bf16(const AttnArgs& a, const AttnSplit& s,
         for (int pos = keys.begin, step = 0; pos < keys.end; pos += 64, ++step) advance(pos, step);
     }
 
-    const float sum = l + __shfl_xor(l, 32);
+    // (a score past fp32, whose difference to the infinite maximum gave the weight 0)
+    const float sum = m == INFINITY ? NAN : l + __shfl_xor(l, 32);
     const int row = wave * 32 + c32;
     if (it.parts > 1) {
         const long slot = (long)it.slot + ((long)it.part * it.tiles + it.tile) * a.Hkv + it.h;

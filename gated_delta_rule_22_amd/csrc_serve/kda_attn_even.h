@@ -292,6 +292,14 @@ __global__ __launch_bounds__(64 * kListWaves) void even_list(A a, AttnSplit s, E
     }
 }
 
+// What joins from a piece, or from the pieces that some lanes have joined. Without weights
+// (scores of -infinity alone) its values are 0, or NaN where a position's are not finite:
+// that has to reach the row.
+__device__ __forceinline__ Joined with_odd(Joined x) {
+    if (x.l == 0.f) x.l = (x.v[0] + x.v[1]) + (x.v[2] + x.v[3]);
+    return x;
+}
+
 // Joins the pieces of the tiles that were cut, their rows shared evenly by the
 // workgroups. Every workgroup reads the descriptions of all G and puts the tiles in
 // order. Up to 16 pieces a group of D / 4 lanes has a row; with more the groups share
@@ -355,8 +363,10 @@ __global__ __launch_bounds__(kAttnThreads) void even_join(A a, EvenSplit e) {
             const long at = (long)slot * e.R + row;
             Joined y;
             y.m = e.ml[at * 2];
-            y.l = in ? e.ml[at * 2 + 1] : 0.f;
+            y.l = e.ml[at * 2 + 1];
             y.v = *(const f32x4*)(e.acc + at * D + d);
+            y = with_odd(y);
+            if (!in) y.l = 0.f;
             return y;
         };
         const auto write = [&](const Joined& y, int row) {
@@ -429,7 +439,7 @@ __global__ __launch_bounds__(kAttnThreads) void even_join(A a, EvenSplit e) {
                     x1.m = lds_ml[g][0];
                     x1.l = lds_ml[g][1];
                     x1.v = *(const f32x4*)&lds_v[g][d];
-                    z.add(x1);
+                    z.add(with_odd(x1));
                 }
                 write(z, row_a + row);
             }

@@ -479,7 +479,7 @@ __device__ __forceinline__ void narrow_run(const AttnArgs& a, const EvenSplit& e
         const float sum = lds.sum[0][y] + lds.sum[1][y], ref = lds.ref[y];
         if (it.pieces > 1) {
             const long at = (long)it.slot * R + y;
-            // (a row without a key in this piece has l = 0, and its values are not used)
+            // (a row without a key in this piece has sums of 0)
 #pragma unroll
             for (int b = 0; b < CT; ++b) *(f32x4*)(e.acc + at * DC + col + 16 * b) = acc[r][b];
             if (vw == 0 && g4 == 0) {
@@ -677,7 +677,7 @@ __device__ __forceinline__ void latent_run_f32(const AttnArgs& a, const EvenSpli
         if (!cut && !x.in) continue;
         const float inv = cut ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
         float* to = cut ? e.acc + at * DC : (float*)a.o + x.q * DC;
-        for (int g = 0; (!cut || sum != 0.f) && g < CT / VW; ++g)
+        for (int g = 0; g < CT / VW; ++g)
             for (int i = 0; i < 4; ++i)
                 for (int j = 0; j < VW; ++j)
                     to[wave * (DC / 4) + 16 * VW * g + VW * (4 * g4 + i) + j] = acc[r][g * VW + j][i] * inv;

@@ -105,9 +105,10 @@ kda_status kda_latent_append(const void* kv, const float* w, const int* slot_map
  * Sums over positions are fp32, of weights up to 2^8: |c| times the number of
  * positions that a row sees is meant to be at most 2^118. Scores (times log2 e) that
  * are past fp32 count as infinite.
- * What masked positions and unused cache rows hold does not reach the result; a
- * row that sees a position that is not finite is not finite, in part or as a
- * whole. dr = 64, dc in {128, 256, 512}; T * Hq, max_pages * page_size and B are
+ * What masked positions and unused cache rows hold does not reach the result. A row
+ * that sees a c that is not finite, or has a score of NaN or +infinity, is not finite,
+ * in part or as a whole; a position of finite c with a score of -infinity has no
+ * weight. dr = 64, dc in {128, 256, 512}; T * Hq, max_pages * page_size and B are
  * at most 2^30.
  */
 size_t kda_attn_latent_workspace_size(int T, int B, int Hq, int dc, int dr, int max_new,

@@ -17,7 +17,7 @@ from typing import Optional, Tuple
 import torch
 
 import gated_delta_rule_22_amd as _kda
-from .serve import _call, _device, _dims, _dtype, _out, _ptr, _workspace
+from .serve import _call, _device, _dims, _dtype, _out, _ptr, _too_large, _workspace
 
 
 class _RopeStruct(ctypes.Structure):
@@ -121,6 +121,8 @@ def kda_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slot_map:
     T, Hq, d = _dims(q, "q", 3)
     pool, Hkv, page, _ = _dims(k_cache, "k_cache", 4)
     B, = _dims(kept_len, "kept_len", 1)
+    if (T | B | pool) >> 31:
+        _too_large("kda_rope_append")
     i32, rows, cache = torch.int32, (T, Hkv, d), (pool, Hkv, page, d)
     if q_out is None:
         q_out = torch.empty_like(q) if stream is None else _kda._empty(q.shape, dt, dev, stream)
@@ -149,6 +151,8 @@ def kda_latent_append(kv: torch.Tensor, slot_map: torch.Tensor, kept_len: torch.
     T, width = _dims(kv, "kv", 2)
     pool, page, _ = _dims(cache, "cache", 3)
     B, = _dims(kept_len, "kept_len", 1)
+    if (T | B) >> 31:
+        _too_large("kda_latent_append")
     i32 = torch.int32
     if (q is None) != (q_out is None):
         raise ValueError("kda_latent_append takes q and q_out together")
@@ -192,6 +196,8 @@ def kda_attn_latent(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
     T, Hq, dk = _dims(q, "q", 3)
     pool, page, _ = _dims(cache, "cache", 3)
     B, width = _dims(block_table, "block_table", 2)
+    if (T | B | width) >> 31:
+        _too_large("kda_attn_latent")
     i32, dr = torch.int32, dk - dc
     o = _out(o, (T, Hq, dc), dt, dev, stream)
     if lse is None and want_lse:
@@ -237,6 +243,8 @@ def kda_attn_expanded(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_
     B = _dims(cu_q, "cu_q", 1)[0] - 1
     if B < 0:
         raise ValueError("cu_q needs B + 1 entries")
+    if (T | N | B) >> 31:
+        _too_large("kda_attn_expanded")
     if k_pe.shape[0] != N or k_pe.dtype is not dt or k_pe.device != dev:
         _kda._check(k_pe, "k_pe", (N, dr), dt, dev)
     # (of a single row, or of none, the stride means nothing)

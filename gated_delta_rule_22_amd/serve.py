@@ -62,6 +62,11 @@ def _dims(t: torch.Tensor, name: str, n: int):
     return shape
 
 
+def _too_large(what: str):
+    """A size that does not fit the library's 32-bit arguments (which would cut it)."""
+    raise ValueError(f"{what}: a size is larger than 2^31 - 1")
+
+
 def _ptr(t: torch.Tensor, name: str, shape, dtype, dev) -> int:
     """The address of a tensor that is as it has to be."""
     if t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
@@ -132,6 +137,8 @@ def kda_page_plan(kept_len: torch.Tensor, n_new: torch.Tensor, n_pages: torch.Te
         raise ValueError("kda_page_plan needs n_slots or slot_map")
     if n_slots is None:
         n_slots, = _dims(slot_map, "slot_map", 1)
+    if max(B, width, pool, n_slots) >> 31:
+        _too_large("kda_page_plan")
     n_pages_out = _out(n_pages_out, (B,), i32, dev, stream)
     ring_out = _out(ring_out, (2,), i32, dev, stream)
     cu_new = _out(cu_new, (B + 1,), i32, dev, stream)
@@ -157,6 +164,8 @@ def kda_cache_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
     dev, dt = _device(k, "kda_cache_append"), _dtype(k)
     T, H, d = _dims(k, "k", 3)
     pool, _, page, _ = _dims(k_cache, "k_cache", 4)
+    if (T | pool) >> 31:
+        _too_large("kda_cache_append")
     rows, cache = (T, H, d), (pool, H, page, d)
     _call("kda_cache_append", dev, stream, _ptr(k, "k", rows, dt, dev), _ptr(v, "v", rows, dt, dev),
           _ptr(slot_map, "slot_map", (T,), torch.int32, dev),
@@ -187,6 +196,8 @@ def kda_attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     T, Hq, d = _dims(q, "q", 3)
     pool, Hkv, page, _ = _dims(k_cache, "k_cache", 4)
     B, width = _dims(block_table, "block_table", 2)
+    if (T | B | width) >> 31:
+        _too_large("kda_attn_paged")
     i32, cache = torch.int32, (pool, Hkv, page, d)
     if o is None:
         o = torch.empty_like(q) if stream is None else _kda._empty(q.shape, dt, dev, stream)
@@ -228,6 +239,8 @@ def kda_draft_verify(target_probs: torch.Tensor, draft_probs: Optional[torch.Ten
     T = T1 - 1
     if T < 0:
         raise ValueError("target_probs needs T + 1 >= 1 rows per request")
+    if (B | T | V) >> 31:
+        _too_large("kda_draft_verify")
     i32 = torch.int32
     n_commit = _out(n_commit, (B,), i32, dev, stream)
     tokens = _out(tokens, (B, T1), i32, dev, stream)

@@ -148,15 +148,18 @@ struct AttnBlock {
         return (long)r0.tiles * r0.kv + (long)r1.tiles * r1.kv +
                ((long)r2.tiles * r2.kv + (long)r3.tiles * r3.kv);
     }
-    // ceil(kv / C) in fp32. C is above the call's work over 2^most_log2, and kv is
-    // part of that work: the quotient is below 2^11, the three roundings in it move
-    // it by far less than 1, and a comparison to either side mends it. (A request
-    // without tiles has no part in the work, and its parts count for nothing.)
+    // ceil(kv / C) in fp32. C is above the call's work over 2^16 (2^most_log2, where the
+    // parts are not kda_attn_even.h's units), and kv is part of that work: the quotient is
+    // at most 2^16, and three roundings of 2^-24 move it by less than 0.012. Cut to a
+    // whole number it may then be two too few, where the quotient is just above a whole
+    // number (from 2^23 keys on), or one too many. (A request without tiles has no part
+    // in the work, and its parts count for nothing.)
     static __device__ int parts(int kv, int C, float rC) {
-        int n = (int)((float)kv * rC);
-        n = max(n, 1);
-        if ((long)n * C < kv) ++n;
-        if ((long)(n - 1) * C >= kv && n > 1) --n;
+        int n = max((int)((float)kv * rC), 1);
+        // (fits 32 bits: two parts or less, and one where a part is more than 2^28 keys)
+        const int rest = (int)((unsigned)kv - (unsigned)n * (unsigned)C);
+        if (rest > 0) n += rest > C ? 2 : 1;
+        if (rest <= -C && n > 1) --n;
         return n;
     }
     __device__ void split(const AttnArgs& a, int C) {

@@ -1,5 +1,6 @@
-// Work split for attention kernels of which a compute unit holds one workgroup:
-// G groups of workgroups, each an even share of the call's keys.
+// Work split for attention kernels that fill the card with one launch: G groups of
+// workgroups, as many as its compute units hold (one or two each), and each an even share of
+// the call's keys.
 //
 // The rows of a request are cut into tiles of R times `side` rows as in
 // kda_attn_sched.h (one KV head). A tile is a number of units: its keys in Cs, behind
@@ -37,10 +38,9 @@ struct EvenSplit {
 
 // Keys of a unit: 64, or what makes the call some 2^16 units. (cost: tiles times keys,
 // and a key more for each tile, so that there are never 2^31 units.)
-constexpr int kUnitKeys = 64, kUnitsLog2 = 16;
+constexpr int kUnitKeys = 64;
 __device__ __forceinline__ int even_unit(long cost) {
     const float want = (float)cost * 0x1p-16f;
-    static_assert(kUnitsLog2 == 16, "");
     return __builtin_amdgcn_readfirstlane(((int)fminf(want, 1073741824.f) & ~(kUnitKeys - 1)) + kUnitKeys);
 }
 // Units without keys: a tile's start costs about what 128 of its keys do.

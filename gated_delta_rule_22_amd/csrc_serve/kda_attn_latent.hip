@@ -14,7 +14,7 @@
 // What bounds it, and what it measured with 512 + 64 channels:
 //   256 single tokens, 16 heads, 2.7 GB of cache: 495 us, 5.5 TB/s, the memory's rate;
 //   128 single tokens, 128 heads, 199 GF: 335 us. Each 64 rows of a request read its keys
-//     again, from the last-level cache if they do it at the same time (`side`);
+//     again, from their XCD's cache if they do it at the same time (`side`);
 //   4 drafts of 8 tokens over up to 262144 keys, 32 heads, 353 GF: 490 us, 720 TF/s, and
 //     1060 with the weights' second terms;
 //   one token over 1000 keys, 32 heads: 20.5 us, of which two launches are 10, and the rest
@@ -37,8 +37,12 @@ __device__ __forceinline__ void wait_loads() {
 }
 
 // Piece of 16 bytes that LDS holds in place of piece c of a key's row. bf16:
-// the rows' stride is 32 banks modulo 64; 16 lanes that read one piece of 16
-// keys, and 32 lanes that read two pieces of 8 keys, cover the banks once.
+// the rows' stride is 32 banks modulo 64; 16 lanes in a row that read one piece of 16
+// keys, and 32 lanes that read two pieces of 8 keys, cover the banks once. The latter
+// (the values) have no conflicts; the former do: SQ_LDS_BANK_CONFLICT counts 320 cycles a
+// step of 32 rows and 352 of 64, 4 for each of its 72 reads of keys and 4 for each store of
+// weights. That is what groups of the lanes 0-3, 12-15, 20-27 and of the others of each 32
+// would cost instead of 16 lanes in a row.
 __device__ __forceinline__ int latent_piece(int key, int c) {
     return c ^ (2 * (key >> 1 & 3) + (key >> 3 & 1));
 }
@@ -158,15 +162,9 @@ struct KeySteps {
         fetched += KT;
         buf = buf + 1 == BUF ? 0 : buf + 1;
     }
-    // Waits for this wave's part of the oldest step, of `after` that may be behind it.
-    __device__ __forceinline__ void wait(int after) {
-        int n = 0;
-#pragma unroll
-        for (int b = 1; b < BUF - 1; ++b) n += b <= after && n == b - 1 && have[b];
-        if (n == 2) {
-            if (fewer) wait_loads<2 * LD - 2>();
-            else wait_loads<2 * LD>();
-        } else if (n == 1) {
+    // Waits for this wave's part of the oldest step, behind which there may be another one.
+    __device__ __forceinline__ void wait() {
+        if (BUF > 3 && have[1]) {
             if (fewer) wait_loads<LD - 1>();
             else wait_loads<LD>();
         } else {
@@ -241,7 +239,7 @@ __device__ __forceinline__ void narrow_run(const AttnArgs& a, const EvenSplit& e
     const auto begin_step = [&](int j, bool& partial) {
         int missing = 0;
         if (j < steps) {
-            ks.wait(BUF - 3);
+            ks.wait();
             missing = ks.take();
         }
         __syncthreads();                             // the step has landed, the weights of the last are there

@@ -180,7 +180,7 @@ kda_status kda_attn_expanded(const void* q, const void* kv, const void* k_pe, co
     if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_UNSUPPORTED;
     if (dr != kda::kPe || dn != dv || (dv != 64 && dv != 128)) return KDA_ERR_UNSUPPORTED;
     if (pe_stride < dr || pe_stride % 8) return KDA_ERR_INVALID_ARG;
-    // (the kernels' offsets over eight keys have 32 bits)
+    // (the kernels' offsets, in bytes over the 16 keys or fewer that a wave fetches, have 32 bits)
     if (pe_stride > kMaxKeyRow || product(H, (size_t)dn + dv) > (size_t)kMaxKeyRow) return KDA_ERR_INVALID_ARG;
     if (T == 0 || B == 0 || H == 0) return KDA_OK;
     const size_t elt = dtype == KDA_BF16 ? 2 : 4;

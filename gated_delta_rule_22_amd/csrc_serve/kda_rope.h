@@ -8,8 +8,6 @@
 namespace kda {
 namespace {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
 constexpr int kRopeWaves = 4;      // of a workgroup
 constexpr int kRopePairs = 64;     // rot is at most 128
 

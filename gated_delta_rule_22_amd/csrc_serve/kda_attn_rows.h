@@ -394,9 +394,9 @@ Launch launch_of(long T, long B, long G, long Hkv, int R, int most_log2, int som
     return l;
 }
 
-// Workgroups of a launch: a grid holds fewer than 2^32 threads, and the calls
-// that are accepted make up to 2^31 parts (one each for T Hq of 2^30).
-constexpr unsigned kGrid = 1u << 23;
+// Workgroups of a launch, of up to 512 threads: a grid holds fewer than 2^32 of them, and
+// the calls that are accepted make up to 2^31 parts (one each for T Hq of 2^30).
+constexpr unsigned kGrid = 1u << 22;
 template <typename F>
 void in_grids(unsigned n, F launch) {
     for (unsigned first = 0; first < n; first += kGrid) launch(n - first < kGrid ? n - first : kGrid, first);

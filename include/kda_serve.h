@@ -118,6 +118,8 @@ kda_status kda_cache_append(const void* k, const void* v, const int* slot_map,
  *   max_new  the largest number of new tokens of one request, 0 = unknown. It
  *            selects kernels only: results are right whatever it says.
  *   ws       kda_attn_paged_workspace_size() bytes
+ * Sums over positions are fp32, of weights up to 2^8: |v| times the number of
+ * positions that a row sees is meant to be at most 2^118.
  * What masked positions and unused cache rows hold (NaN and infinities
  * included) does not reach the result. d, page_size and dtype as above.
  */

@@ -251,6 +251,8 @@ def kda_prefill_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         raise ValueError("kda_prefill_varlen needs GPU tensors")
     if N < 0:
         raise ValueError("cu_seqlens needs N + 1 >= 1 entries")
+    if (N | T) >> 31:
+        raise ValueError("kda_prefill_varlen: a size is larger than 2^31 - 1")
     dt = q.dtype
     if dt not in _DTYPES:
         raise ValueError(f"unsupported dtype {dt}")

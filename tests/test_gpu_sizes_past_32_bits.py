@@ -64,6 +64,13 @@ def test_plan_and_vocabulary(many):
                              torch.zeros((1, 1), device=DEV))
 
 
+def test_sequences(many):
+    q, k, v = (torch.zeros((64, 1, 16), dtype=BF, device=DEV) for _ in range(3))
+    gate, beta = torch.zeros((64, 1, 16), device=DEV), torch.zeros((64, 1), device=DEV)
+    with pytest.raises(ValueError):
+        kda.kda_prefill_varlen(q, k, v, gate, beta, many[:MANY + 1], want_state=False)
+
+
 def test_tokens(many):
     # rows of no heads take no memory, and a slot each
     slots = many[:MANY]
